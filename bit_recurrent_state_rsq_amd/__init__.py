@@ -25,7 +25,8 @@ from . import codec
 from .accounting import step_bytes_per_tile, workload_step_bytes, workload_merge_bytes
 
 __all__ = ["State", "Error", "state_bytes", "make_config", "step_bytes_per_tile",
-           "workload_step_bytes", "workload_merge_bytes", "allocate_head_bits", "ErrorAccounting"]
+           "workload_step_bytes", "workload_merge_bytes", "allocate_head_bits", "ErrorAccounting",
+           "causal_conv", "causal_conv_step", "ssm_scan", "ssm_step", "rms_norm", "W4Weight", "w4_linear"]
 
 
 def make_config(model, batch, heads, d_k, d_v, group, bits=4, head_bits=None,
@@ -389,3 +390,5 @@ class State:
 
 
 from .diagnostics import ErrorAccounting  # noqa: E402
+from .layer import (causal_conv, causal_conv_step, ssm_scan, ssm_step, rms_norm,  # noqa: E402
+                    W4Weight, w4_linear)

@@ -25,15 +25,18 @@ RETNET, MAMBA2, GLA, GDN = 0, 1, 2, 3
 MODELS = {"retnet": RETNET, "mamba2": MAMBA2, "gla": GLA, "gdn": GDN}
 SCALE_DYNAMIC, SCALE_PERSISTENT, SCALE_YOKED = 0, 1, 2
 SCALE_MODES = {"dynamic": SCALE_DYNAMIC, "persistent": SCALE_PERSISTENT, "yoked": SCALE_YOKED}
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, INT8, E4M3 = 0, 1, 2, 3, 4
 DTYPES = {"f32": F32, "f16": F16, "bf16": BF16}
 INIT_ZERO, ATTACH = 0, 1
+ACT_NONE, ACT_SILU = 0, 1
 F_NONFINITE, F_SCALE_OVERFLOW, F_CLIPPED = 1, 2, 4
 
 EXPORTS = ["rsq_state_bytes", "rsq_state_alloc", "rsq_state_free", "rsq_state_layout",
            "rsq_tile_sections", "rsq_state_counters", "rsq_decode_step", "rsq_decode_step_timed",
            "rsq_decode_step_diag", "rsq_merge_bypass", "rsq_merge_bypass_timed",
-           "rsq_readout", "rsq_get_status", "rsq_last_error", "rsq_abi_version", "rsq_allocate_head_bits"]
+           "rsq_readout", "rsq_get_status", "rsq_last_error", "rsq_abi_version", "rsq_allocate_head_bits",
+           "rsq_causal_conv", "rsq_ssm_scan_workspace", "rsq_ssm_scan", "rsq_ssm_step", "rsq_rms_norm",
+           "rsq_w4_bytes", "rsq_w4_pack", "rsq_w4_linear"]
 
 
 class Config(ctypes.Structure):
@@ -61,6 +64,35 @@ class Layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("header", "status", "head_table", "tiles", "batch_stride", "tile_codes",
                  "tile_scales", "tile_bypass_u", "tile_bypass_w", "tile_ref", "total")]
+
+
+_P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class Conv(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("dtype", "seqs", "channels", "width", "activation")]
+                + [("tokens", _I64), ("max_len", _I64), ("offsets", _P), ("x", _P), ("x_stride", _I64),
+                   ("weight", _P), ("bias", _P), ("state", _P), ("y", _P), ("y_stride", _I64)])
+
+
+class Ssm(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("dtype", "seqs", "heads", "groups", "d_k", "d_v", "softplus", "state_in")]
+                + [("tokens", _I64), ("max_len", _I64), ("offsets", _P), ("x", _P), ("x_stride", _I64), ("B", _P),
+                   ("b_stride", _I64), ("C", _P), ("c_stride", _I64), ("dt", _P), ("dt_stride", _I64), ("A", _P),
+                   ("D", _P), ("dt_bias", _P), ("state", _P), ("y", _P), ("y_stride", _I64), ("workspace", _P),
+                   ("workspace_bytes", ctypes.c_size_t)])
+
+
+class Norm(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("dtype", "out_dtype", "cols", "group")]
+                + [("eps", _F), ("rows", _I64), ("x", _P), ("x_stride", _I64), ("residual", _P),
+                   ("residual_stride", _I64), ("weight", _P), ("y", _P), ("y_stride", _I64), ("scales", _P)])
+
+
+class W4(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("x_dtype", "out_dtype", "m", "n", "k", "group", "scale_dtype", "x_group")]
+                + [("x", _P), ("x_stride", _I64), ("x_scale", _P), ("packed", _P),
+                   ("packed_bytes", ctypes.c_size_t), ("y", _P), ("y_stride", _I64)])
 
 
 class Error(RuntimeError):
@@ -98,6 +130,14 @@ def _load():
         "rsq_abi_version": (I32, []),
         "rsq_allocate_head_bits": (I32, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float), I32,
                                          ctypes.c_float, ctypes.POINTER(I32)]),
+        "rsq_causal_conv": (I32, [ctypes.POINTER(Conv), P]),
+        "rsq_ssm_scan_workspace": (I32, [ctypes.POINTER(Ssm), ctypes.POINTER(SZ)]),
+        "rsq_ssm_scan": (I32, [ctypes.POINTER(Ssm), P]),
+        "rsq_ssm_step": (I32, [ctypes.POINTER(Ssm), P]),
+        "rsq_rms_norm": (I32, [ctypes.POINTER(Norm), P]),
+        "rsq_w4_bytes": (I32, [I32, I32, I32, I32, ctypes.POINTER(SZ)]),
+        "rsq_w4_pack": (I32, [P, P, I32, I32, I32, I32, P, SZ, P]),
+        "rsq_w4_linear": (I32, [ctypes.POINTER(W4), P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

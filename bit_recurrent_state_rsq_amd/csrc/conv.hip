@@ -1,0 +1,308 @@
+// Short causal convolution of every channel, before a selective scan:
+//   y[t, c] = act(bias[c] + sum_{j < W} w[c, j] x[t - W + 1 + j, c]),  W = 2..4,
+// act = silu or nothing. Inputs before a sequence's first come from its state
+// [channels][W - 1] (oldest first; none: zeros), which takes the last W - 1
+// inputs afterwards.
+//
+// A read and a write of every element against 2 W operations: bound by memory.
+// A lane owns 16 bytes of consecutive channels, so that a wavefront reads 1 KB
+// runs, and walks kTile tokens with the last W - 1 inputs in registers; a tile
+// reads W - 1 rows again (from L2). The rows of a tile are loaded kAhead at a
+// time before the first is used.
+#include <type_traits>
+
+#include "host_util.hpp"
+#include "layer_ops.hpp"
+
+namespace rsq {
+namespace {
+
+constexpr int kTile = 32;   // tokens of a wavefront
+constexpr int kAhead = 8;   // rows in flight
+constexpr int kWaves = 4;   // wavefronts of a block, each with a tile of its own
+
+struct ConvArgs {
+  const void* x;
+  void* y;
+  void* state;
+  const float* weight;
+  const float* bias;
+  int64_t x_stride, y_stride;
+  Sequences q;
+  int32_t C;
+  int32_t cblocks, tiles;   // blocks along the channels; blocks along a sequence
+};
+
+// exp(-v) saturates to infinity for v below about -88, where silu(v) rounds to
+// -0. bf16 results take the hardware's exp2 and reciprocal (their errors, a few
+// 2^-23, vanish in the rounding to 8 bits); fp32 ones the exact division.
+template <typename T>
+__device__ __forceinline__ float silu(float v) {
+  if constexpr (std::is_same<T, float>::value) return v / (1.f + expf(-v));
+  else return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+}
+
+template <typename T, int W, int VEC, bool SILU>
+__device__ __forceinline__ void conv_out(const float (&win)[W][VEC], const float (&w)[VEC][W], const float (&b)[VEC],
+                                         float (&out)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    float acc = b[e];
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc = __builtin_fmaf(w[e][j], win[j][e], acc);
+    out[e] = SILU ? silu<T>(acc) : acc;
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_row(const T* p, float (&v)[VEC]) {
+  if constexpr (VEC == 1) v[0] = to_f32(p[0]);
+  else load_vec<VEC>(p, v);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_row(T* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) from_f32(v[0], p[0]);
+  else store_vec<VEC>(p, v);
+}
+
+// weights of VEC channels ([channel][tap], so VEC * W consecutive floats) and their biases
+template <int W, int VEC>
+__device__ __forceinline__ void load_params(const ConvArgs& a, int c, float (&w)[VEC][W], float (&b)[VEC]) {
+  if constexpr (VEC == 1) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[0][j] = a.weight[(size_t)c * W + j];
+    b[0] = a.bias ? a.bias[c] : 0.f;
+  } else {
+    float flat[VEC * W];
+    load_vec<VEC * W>(a.weight + (size_t)c * W, flat);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[e][j] = flat[e * W + j];
+    if (a.bias) load_vec<VEC>(a.bias + c, b);
+    else
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) b[e] = 0.f;
+  }
+}
+
+// The state of VEC channels: VEC (W - 1) consecutive elements, h[j] the input
+// W - 1 - j before the sequence.
+template <typename T, int W, int VEC>
+__device__ __forceinline__ void load_state(const T* p, float (&h)[W - 1][VEC]) {
+  float flat[VEC * (W - 1)];
+  if constexpr (VEC == 1) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) flat[j] = to_f32(p[j]);
+  } else {
+    load_vec<VEC*(W - 1)>(p, flat);
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) h[j][e] = flat[e * (W - 1) + j];
+}
+
+template <typename T, int W, int VEC>
+__device__ __forceinline__ void store_state(T* p, const float (&h)[W - 1][VEC]) {
+  float flat[VEC * (W - 1)];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) flat[e * (W - 1) + j] = h[j][e];
+  if constexpr (VEC == 1) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) from_f32(flat[j], p[j]);
+  } else {
+    store_vec<VEC*(W - 1)>(p, flat);
+  }
+}
+
+template <typename T, int W, int VEC, bool SILU>
+__global__ __launch_bounds__(64 * kWaves) void conv_prompt_kernel(ConvArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t id = blockIdx.x;
+  const int cb = (int)(id % a.cblocks);
+  id /= a.cblocks;
+  const int64_t tile = id % a.tiles;
+  const int s = (int)(id / a.tiles);
+  int64_t len;
+  const int64_t begin = seq_range(a.q, s, len);
+  const int64_t t0 = (tile * kWaves + wave) * kTile;
+  const int c = (cb * 64 + lane) * VEC;
+  if (c >= a.C || t0 >= len) return;   // (an empty sequence keeps its state)
+  const T* x = reinterpret_cast<const T*>(a.x) + begin * a.x_stride + c;
+  T* y = reinterpret_cast<T*>(a.y) + begin * a.y_stride + c;
+  T* st = a.state ? reinterpret_cast<T*>(a.state) + ((size_t)s * a.C + c) * (W - 1) : nullptr;
+  float w[VEC][W], b[VEC];
+  load_params<W, VEC>(a, c, w, b);
+  float win[W][VEC];   // win[W - 1] is the current input
+  float old[W - 1][VEC];
+  if (t0 == 0) {
+    if (st) load_state<T, W, VEC>(st, old);
+    else
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) old[j][e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) win[j][e] = old[j][e];
+  } else {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) load_row<T, VEC>(x + (t0 - (W - 1) + j) * a.x_stride, win[j]);
+  }
+  const int n = (int)(len - t0 < kTile ? len - t0 : kTile);
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    float rows[kAhead][VEC];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i < n) load_row<T, VEC>(x + (t0 + i0 + i) * a.x_stride, rows[i]);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i < n) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) win[W - 1][e] = rows[i][e];
+        float out[VEC];
+        conv_out<T, W, VEC, SILU>(win, w, b, out);
+        store_row<T, VEC>(y + (t0 + i0 + i) * a.y_stride, out);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+      }
+    }
+  }
+  // The lane of the first tile is the only reader of this state, and it has
+  // read it: it writes the new one too. Inputs t < 0 are the old state's.
+  if (t0 == 0 && st) {
+    float next[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int64_t t = len - (W - 1) + j;
+      if (t >= 0) {
+        load_row<T, VEC>(x + t * a.x_stride, next[j]);
+      } else {
+        // t + W - 1 = len + j with 0 < len < W - 1
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+          if (k == (int)(len + j))
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) next[j][e] = old[k][e];
+      }
+    }
+    store_state<T, W, VEC>(st, next);
+  }
+}
+
+// One token of every sequence: a lane per VEC channels of a sequence. The state
+// (W - 1 inputs a channel, read and written) is most of the traffic.
+template <typename T, int W, int VEC, bool SILU>
+__global__ __launch_bounds__(256) void conv_token_kernel(ConvArgs a) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int cv = (a.C + VEC - 1) / VEC;
+  const int64_t s = id / cv;
+  if (s >= a.q.seqs) return;
+  const int c = (int)(id - s * cv) * VEC;
+  T* st = a.state ? reinterpret_cast<T*>(a.state) + ((size_t)s * a.C + c) * (W - 1) : nullptr;
+  float win[W][VEC], h[W - 1][VEC], w[VEC][W], b[VEC], out[VEC];
+  load_row<T, VEC>(reinterpret_cast<const T*>(a.x) + s * a.x_stride + c, win[W - 1]);
+  if (st) load_state<T, W, VEC>(st, h);
+  else
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) h[j][e] = 0.f;
+  load_params<W, VEC>(a, c, w, b);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) win[j][e] = h[j][e];
+  conv_out<T, W, VEC, SILU>(win, w, b, out);
+  store_row<T, VEC>(reinterpret_cast<T*>(a.y) + s * a.y_stride + c, out);
+  if (st) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) h[j][e] = win[j + 1][e];
+    store_state<T, W, VEC>(st, h);
+  }
+}
+
+typedef void (*ConvFn)(ConvArgs);
+
+template <typename T, int W, int VEC>
+ConvFn pick(bool token, bool silu) {
+  if (token) return silu ? conv_token_kernel<T, W, VEC, true> : conv_token_kernel<T, W, VEC, false>;
+  return silu ? conv_prompt_kernel<T, W, VEC, true> : conv_prompt_kernel<T, W, VEC, false>;
+}
+
+template <typename T, int VEC>
+ConvFn pick_width(int width, bool token, bool silu) {
+  switch (width) {
+    case 2: return pick<T, 2, VEC>(token, silu);
+    case 3: return pick<T, 3, VEC>(token, silu);
+    default: return pick<T, 4, VEC>(token, silu);
+  }
+}
+
+}  // namespace
+}  // namespace rsq
+
+using namespace rsq;
+
+extern "C" rsq_status rsq_causal_conv(const rsq_conv* p, void* stream) {
+  if (!p) return fail(RSQ_E_INVALID, "conv is NULL");
+  if (p->dtype != RSQ_F32 && p->dtype != RSQ_BF16) return fail(RSQ_E_INVALID, "dtype %d", p->dtype);
+  if (p->activation != RSQ_ACT_NONE && p->activation != RSQ_ACT_SILU)
+    return fail(RSQ_E_INVALID, "activation %d", p->activation);
+  if (p->seqs < 1 || p->channels < 1) return fail(RSQ_E_INVALID, "seqs %d channels %d", p->seqs, p->channels);
+  if (p->width < 2 || p->width > 4) return fail(RSQ_E_UNSUPPORTED, "width %d not in 2..4", p->width);
+  if (p->tokens < 0 || p->tokens > 0x7fffffff) return fail(RSQ_E_INVALID, "tokens %lld", (long long)p->tokens);
+  if (p->max_len < 0 || p->max_len > p->tokens) return fail(RSQ_E_INVALID, "max_len %lld of %lld tokens",
+                                                            (long long)p->max_len, (long long)p->tokens);
+  if (!p->offsets && p->tokens != p->max_len * p->seqs)
+    return fail(RSQ_E_INVALID, "without offsets every sequence has max_len rows: %lld tokens, %d of %lld",
+                (long long)p->tokens, p->seqs, (long long)p->max_len);
+  if (p->max_len == 0) return RSQ_OK;
+  if (!p->x || !p->weight || !p->y) return fail(RSQ_E_INVALID, "x, weight and y must be non-NULL");
+  if (p->x_stride < p->channels || p->y_stride < p->channels)
+    return fail(RSQ_E_INVALID, "row strides %lld, %lld below %d channels", (long long)p->x_stride,
+                (long long)p->y_stride, p->channels);
+  const int size = p->dtype == RSQ_BF16 ? 2 : 4;
+  if (!aligned(p->x, size) || !aligned(p->y, size) || !aligned(p->state, size) || !aligned(p->weight, 4) ||
+      !aligned(p->bias, 4) || !aligned(p->offsets, 4))
+    return fail(RSQ_E_INVALID, "a pointer is not aligned to its element type");
+  const int64_t C = p->channels;
+  const Span written[] = {{p->y, span_bytes(p->tokens, p->y_stride, C, size), "y"},
+                          {p->state, (int64_t)p->seqs * C * (p->width - 1) * size, "state"}};
+  const Span read[] = {{p->x, span_bytes(p->tokens, p->x_stride, C, size), "x"},
+                       {p->weight, C * p->width * 4, "weight"},
+                       {p->bias, C * 4, "bias"},
+                       {p->offsets, (int64_t)(p->seqs + 1) * 4, "offsets"}};
+  if (const rsq_status s = check_overlap(written, read)) return s;
+
+  // 16-byte accesses where every row, parameter and state address allows them,
+  // one element at a time otherwise
+  const int vec = 16 / size;
+  const bool wide = C % vec == 0 && p->x_stride % vec == 0 && p->y_stride % vec == 0 && aligned(p->x, 16) &&
+                    aligned(p->y, 16) && aligned(p->state, 16) && aligned(p->weight, 16) && aligned(p->bias, 16);
+  const int v = wide ? vec : 1;
+  const bool token = !p->offsets && p->max_len == 1, silu = p->activation == RSQ_ACT_SILU;
+  ConvArgs a{};
+  a.x = p->x, a.y = p->y, a.state = p->state, a.weight = p->weight, a.bias = p->bias;
+  a.x_stride = p->x_stride, a.y_stride = p->y_stride;
+  a.q = Sequences{p->offsets, p->tokens, p->max_len, p->seqs};
+  a.C = p->channels;
+  a.cblocks = (int32_t)ceil_div(C, 64 * v);
+  a.tiles = (int32_t)ceil_div(p->max_len, kTile * kWaves);
+  const int64_t blocks = token ? ceil_div(p->seqs * ceil_div(C, v), 256) : (int64_t)a.cblocks * a.tiles * p->seqs;
+  if (blocks > kMaxGrid) return fail(RSQ_E_UNSUPPORTED, "%lld workgroups", (long long)blocks);
+  ConvFn fn;
+  if (p->dtype == RSQ_BF16) fn = wide ? pick_width<Bf16, 8>(p->width, token, silu) : pick_width<Bf16, 1>(p->width, token, silu);
+  else fn = wide ? pick_width<float, 4>(p->width, token, silu) : pick_width<float, 1>(p->width, token, silu);
+  hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * kWaves), 0, (hipStream_t)stream, a);
+  return launched("causal convolution");
+}

@@ -17,14 +17,21 @@
 #include <vector>
 
 #include "rsq.h"
+#include "host_util.hpp"
 #include "rsq_kernels.hpp"
 
+using rsq::fail;
 using rsq::HeadEntry;
+using rsq::hip_fail;
 using rsq::StepArgs;
 
 namespace {
 
 thread_local std::string g_err = "no error";
+
+}  // namespace
+
+namespace rsq {
 
 rsq_status fail(rsq_status code, const char* fmt, ...) {
   char buf[512];
@@ -39,6 +46,10 @@ rsq_status fail(rsq_status code, const char* fmt, ...) {
 rsq_status hip_fail(hipError_t e, const char* what) {
   return fail(RSQ_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace rsq
+
+namespace {
 
 constexpr uint32_t kMagicHdr = 0x31515352u;  // 'RSQ1'
 constexpr size_t kAlign = 256;

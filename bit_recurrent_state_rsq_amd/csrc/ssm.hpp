@@ -1,0 +1,51 @@
+// Arguments and gates of the selective state-space recurrence
+//   d = softplus(dt + dt_bias) (or dt + dt_bias),  a = exp(d A),
+//   S_t = a S_{t-1} + d B_t x_t^T,   y_t = S_t^T C_t + D x_t,
+// shared by the prompt scan and its single-token forms. Heads h of a group
+// g = h / (heads / groups) share B and C.
+#pragma once
+#include "layer_ops.hpp"
+
+namespace rsq {
+
+struct SsmArgs {
+  const void* x;
+  const void* B;
+  const void* C;
+  const void* dt;
+  const float* A;
+  const float* D;
+  const float* dt_bias;
+  float* state;
+  void* y;
+  int64_t x_stride, b_stride, c_stride, dt_stride, y_stride;
+  Sequences q;
+  int32_t H, per_group;   // heads, heads of a group
+  int32_t dk, dv;
+  int32_t softplus, state_in;
+};
+
+// log(1 + e^z) without overflow: max(z, 0) + log1p(e^-|z|)
+__device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
+
+template <typename T>
+__device__ __forceinline__ float ssm_delta(const SsmArgs& a, int64_t row, int h) {
+  float z = to_f32(reinterpret_cast<const T*>(a.dt)[row * a.dt_stride + h]);
+  if (a.dt_bias) z += a.dt_bias[h];
+  return a.softplus ? softplus(z) : z;
+}
+
+}  // namespace rsq
+
+// ---------------------------------------------------------------- host side
+#include "host_util.hpp"
+
+namespace rsq {
+
+// Shapes, types and strides of a scan (`prompt`) or a single-token step.
+rsq_status check_ssm(const rsq_ssm* p, bool prompt);
+// Pointers: present, aligned, outputs apart from everything else.
+rsq_status check_ssm_memory(const rsq_ssm* p);
+SsmArgs ssm_args(const rsq_ssm* p);
+
+}  // namespace rsq

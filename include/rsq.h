@@ -62,8 +62,10 @@ enum {
 enum { RSQ_RETNET = 0, RSQ_MAMBA2 = 1, RSQ_GLA = 2, RSQ_GDN = 3 };
 /* Scale policies (abstract of "When Dynamic Scaling Fails ..."). */
 enum { RSQ_SCALE_DYNAMIC = 0, RSQ_SCALE_PERSISTENT = 1, RSQ_SCALE_YOKED = 2 };
-/* Element types. */
-enum { RSQ_F32 = 0, RSQ_F16 = 1, RSQ_BF16 = 2 };
+/* Element types. INT8 and E4M3 (OCP, saturating) are 8-bit codes with scales. */
+enum { RSQ_F32 = 0, RSQ_F16 = 1, RSQ_BF16 = 2, RSQ_INT8 = 3, RSQ_E4M3 = 4 };
+/* Activations of rsq_causal_conv. */
+enum { RSQ_ACT_NONE = 0, RSQ_ACT_SILU = 1 };
 /* rsq_state_alloc modes. */
 enum { RSQ_INIT_ZERO = 0, RSQ_ATTACH = 1 };
 /* Device status bits (rsq_get_status). */
@@ -313,6 +315,158 @@ rsq_status rsq_get_status(rsq_state* st, uint32_t* flags, void* stream);
  */
 rsq_status rsq_allocate_head_bits(const float* decay_sq, const float* range, int32_t heads,
                                   float mean_bits, int32_t* bits_out);
+
+/* ------------------------------------------------------------------------
+ * Operators of the layer around the decode step. Activations are fp32 or bf16
+ * (`dtype`), parameters fp32; rows are `*_stride` elements apart, with their
+ * elements contiguous. Sums, norms and states are fp32. An output that overlaps
+ * another argument's memory is refused. Every call can be captured in a graph
+ * and replayed.
+ *
+ * Sequences of a prompt batch are packed: `tokens` rows in all, sequence s at
+ * rows offsets[s] .. offsets[s + 1] - 1 (device int32 [seqs + 1]), none longer
+ * than max_len. offsets NULL: every sequence has max_len rows, tokens = seqs *
+ * max_len. Empty sequences are allowed. Offsets live on the device, so they are
+ * not checked on the host: the kernels clamp them into [0, tokens], and of a
+ * sequence longer than max_len only its first max_len rows are taken. Rows of y
+ * that belong to no sequence are left as they were.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Short causal convolution of each channel (before a selective scan):
+ *   y[t, c] = act(bias[c] + sum_{j < width} weight[c, j] x[t - width + 1 + j, c])
+ *   dtype      RSQ_F32 | RSQ_BF16: x, y, state
+ *   width      2..4 (others RSQ_E_UNSUPPORTED)
+ *   weight     device fp32 [channels][width], the last tap on the current token
+ *   bias       device fp32 [channels], or NULL
+ *   state      device [seqs][channels][width - 1] of dtype, oldest input first:
+ *              the inputs before each sequence, replaced by its last width - 1
+ *              inputs (an empty sequence keeps its own); NULL: zeros, none kept
+ * One token of every sequence (offsets NULL, max_len 1) is the decode form.
+ */
+typedef struct rsq_conv {
+  int32_t dtype, seqs, channels, width, activation;
+  int64_t tokens, max_len;
+  const int32_t* offsets;
+  const void* x;
+  int64_t x_stride;
+  const float* weight;
+  const float* bias;
+  void* state;
+  void* y;
+  int64_t y_stride;
+} rsq_conv;
+rsq_status rsq_causal_conv(const rsq_conv* conv, void* stream);
+
+/*
+ * Selective state-space recurrence (the Mamba2 row of Table 1 with its gates):
+ *   delta = softplus(dt + dt_bias), or dt + dt_bias when softplus is 0
+ *   S     = exp(delta A[h]) S + delta B x^T          (S: d_k x d_v, fp32)
+ *   y     = S^T C + D[h] x
+ * for every head h; heads are split evenly over `groups`, and the heads of a
+ * group share B and C.
+ *   dtype      RSQ_F32 | RSQ_BF16: x, B, C, dt, y
+ *   x, y       device [tokens][heads][d_v];  B, C device [tokens][groups][d_k]
+ *   dt         device [tokens][heads]
+ *   A          device fp32 [heads] (negative for a decay)
+ *   D, dt_bias device fp32 [heads], or NULL
+ *   state      device fp32 [seqs][heads][d_k][d_v], replaced by the state after
+ *              each sequence. state_in 0: start from zero, the contents are not
+ *              read; 1: start from the contents (an empty sequence keeps them)
+ *   workspace  rsq_ssm_scan_workspace bytes, 16-byte aligned (scan only; it may
+ *              be NULL when that is 0). Its contents need not be kept.
+ * x, B, C, y and state are 16-byte aligned, the strides of x, B, C and y
+ * multiples of 16 bytes; d_k and d_v are multiples of 8.
+ * rsq_ssm_scan takes d_k <= 256 (bf16) or 128 (fp32). bf16: products take bf16
+ * factors (S and the token weights are rounded to bf16 where they enter y; the
+ * state itself is exact to fp32). An infinite or NaN x makes its column NaN
+ * from its token on; earlier tokens are not touched.
+ * rsq_ssm_step takes one row of every sequence: offsets NULL, max_len 1; d_v <=
+ * 1024, d_k <= 4096.
+ */
+typedef struct rsq_ssm {
+  int32_t dtype, seqs, heads, groups, d_k, d_v;
+  int32_t softplus, state_in;
+  int64_t tokens, max_len;
+  const int32_t* offsets;
+  const void* x;
+  int64_t x_stride;
+  const void* B;
+  int64_t b_stride;
+  const void* C;
+  int64_t c_stride;
+  const void* dt;
+  int64_t dt_stride;
+  const float* A;
+  const float* D;
+  const float* dt_bias;
+  float* state;
+  void* y;
+  int64_t y_stride;
+  void* workspace;
+  size_t workspace_bytes;
+} rsq_ssm;
+rsq_status rsq_ssm_scan_workspace(const rsq_ssm* ssm, size_t* bytes);
+rsq_status rsq_ssm_scan(const rsq_ssm* ssm, void* stream);
+rsq_status rsq_ssm_step(const rsq_ssm* ssm, void* stream);
+
+/*
+ * Root-mean-square norm of rows:
+ *   h = x + residual (stored back to residual, rounded to dtype; residual NULL: h = x)
+ *   y = h / sqrt(mean(h^2) + eps) * weight, of the fp32 h
+ *   dtype      RSQ_F32 | RSQ_BF16: x, residual
+ *   out_dtype  RSQ_F32 | RSQ_BF16, or RSQ_INT8 | RSQ_E4M3: codes round(y / scale),
+ *              nearest-even, with scale = absmax(y) / qmax (127 or 448); a zero
+ *              scale stores code 0
+ *   group      0: a scale per row; 32, 64 or 128 dividing cols: one per group
+ *   scales     device fp32 [rows][cols / group] (group 0: [rows]); NULL without codes
+ *   cols       at most 32768
+ */
+typedef struct rsq_norm {
+  int32_t dtype, out_dtype, cols, group;
+  float eps;
+  int64_t rows;
+  const void* x;
+  int64_t x_stride;
+  void* residual;
+  int64_t residual_stride;
+  const float* weight;
+  void* y;
+  int64_t y_stride;
+  float* scales;
+} rsq_norm;
+rsq_status rsq_rms_norm(const rsq_norm* norm, void* stream);
+
+/*
+ * Products with 4-bit weights: y[m, n] = sum_j x[m, j] codes[n, j] scales[n, j / group].
+ *   group        32, 64 or 128, dividing k
+ *   codes        device int8 [n][k], values -8..7 (their low four bits are taken)
+ *   scales       device [n][k / group] of scale_dtype (RSQ_F32 | RSQ_F16)
+ * rsq_w4_pack lays both out once into `packed` (rsq_w4_bytes bytes, 16-byte
+ * aligned): 16 rows x 128 columns in 1 KB, rows and columns padded with zeros,
+ * then the scales [k / group][n].
+ *   x_dtype      RSQ_F32 | RSQ_BF16, or RSQ_INT8 | RSQ_E4M3 with x_scale
+ *   x_scale      device fp32 [m] (x_group 0) or [m][k / group] (x_group = group);
+ *                NULL without 8-bit x
+ *   out_dtype    RSQ_F32 | RSQ_BF16
+ * Sums are fp32 (int8: int32 inside a group). Meant for few rows: every 16 to 64
+ * rows of x read the weights once. fp32 and bf16 x may reach 2^100 (beyond, the
+ * offset that codes carry inside may overflow).
+ */
+rsq_status rsq_w4_bytes(int32_t n, int32_t k, int32_t group, int32_t scale_dtype, size_t* bytes);
+rsq_status rsq_w4_pack(const int8_t* codes, const void* scales, int32_t n, int32_t k, int32_t group,
+                       int32_t scale_dtype, void* packed, size_t packed_bytes, void* stream);
+typedef struct rsq_w4 {
+  int32_t x_dtype, out_dtype, m, n, k, group, scale_dtype, x_group;
+  const void* x;
+  int64_t x_stride;
+  const float* x_scale;
+  const void* packed;
+  size_t packed_bytes;
+  void* y;
+  int64_t y_stride;
+} rsq_w4;
+rsq_status rsq_w4_linear(const rsq_w4* w4, void* stream);
 
 /* Thread-local description of the last error (never NULL). */
 const char* rsq_last_error(void);
