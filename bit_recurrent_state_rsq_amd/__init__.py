@@ -251,6 +251,21 @@ class State:
                 check(code)
         return issue
 
+    def load_dense(self, dense, stream=None):
+        """Take a dense fp32 state [batch, heads, d_k, d_v] (a scan's) as the first one (rsq_state_load)."""
+        torch = _torch()
+        shape = (self.batch, self.heads, self.d_k, self.d_v)
+        if dense is None:
+            raise ValueError("dense is required")
+        p = self._ptr(dense, torch.float32, shape, "dense")
+        with _layer.On(self.device, stream) as on:
+            check(lib.rsq_state_load(self.h, p, on.ptr))
+
+    def ssm_step(self, x, dt, A, B, C, D=None, dt_bias=None, softplus=False, out=None, stream=None):
+        """One token of a Mamba2 layer on this state (rsq_decode_ssm_step): the arguments of the
+        package's ssm_step, of in_dtype. Returns y [batch, heads, d_v] of x's type."""
+        return _layer.state_ssm_step(self, x, dt, A, B, C, D, dt_bias, softplus, out, stream)
+
     def merge_bypass(self, stream=None, start_event=None, stop_event=None):
         """rsq_merge_bypass; with events, rsq_merge_bypass_timed (recorded by
         the merge kernel's own dispatch)."""
@@ -390,5 +405,6 @@ class State:
 
 
 from .diagnostics import ErrorAccounting  # noqa: E402
+from . import layer as _layer  # noqa: E402
 from .layer import (causal_conv, causal_conv_step, ssm_scan, ssm_step, rms_norm,  # noqa: E402
                     W4Weight, w4_linear)

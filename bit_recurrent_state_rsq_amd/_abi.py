@@ -36,7 +36,8 @@ EXPORTS = ["rsq_state_bytes", "rsq_state_alloc", "rsq_state_free", "rsq_state_la
            "rsq_decode_step_diag", "rsq_merge_bypass", "rsq_merge_bypass_timed",
            "rsq_readout", "rsq_get_status", "rsq_last_error", "rsq_abi_version", "rsq_allocate_head_bits",
            "rsq_causal_conv", "rsq_ssm_scan_workspace", "rsq_ssm_scan", "rsq_ssm_step", "rsq_rms_norm",
-           "rsq_w4_bytes", "rsq_w4_pack", "rsq_w4_linear"]
+           "rsq_w4_bytes", "rsq_w4_pack", "rsq_w4_linear", "rsq_state_load", "rsq_decode_ssm_workspace",
+           "rsq_decode_ssm_step"]
 
 
 class Config(ctypes.Structure):
@@ -138,6 +139,9 @@ def _load():
         "rsq_w4_bytes": (I32, [I32, I32, I32, I32, ctypes.POINTER(SZ)]),
         "rsq_w4_pack": (I32, [P, P, I32, I32, I32, I32, P, SZ, P]),
         "rsq_w4_linear": (I32, [ctypes.POINTER(W4), P]),
+        "rsq_state_load": (I32, [P, P, P]),
+        "rsq_decode_ssm_workspace": (I32, [P, ctypes.POINTER(SZ)]),
+        "rsq_decode_ssm_step": (I32, [P, ctypes.POINTER(Ssm), P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -19,6 +19,7 @@
 #include "rsq.h"
 #include "host_util.hpp"
 #include "rsq_kernels.hpp"
+#include "ssm.hpp"
 
 using rsq::fail;
 using rsq::HeadEntry;
@@ -32,6 +33,9 @@ thread_local std::string g_err = "no error";
 }  // namespace
 
 namespace rsq {
+
+// state_load.hip
+rsq_status launch_state_load(const StepArgs& a, int tiles, const float* dense, bool bits32, bool yoked, void* stream);
 
 rsq_status fail(rsq_status code, const char* fmt, ...) {
   char buf[512];
@@ -642,6 +646,89 @@ rsq_status rsq_readout(const rsq_state* st, const void* q, float* o, void* strea
   a.o = o;
   rsq::DecodeFn fn = rsq::readout_kernel_for(st->geo.cl);
   return launch(fn, st, a, stream);
+}
+
+rsq_status rsq_state_load(rsq_state* st, const float* dense, void* stream) {
+  if (!st) return fail(RSQ_E_INVALID, "state is NULL");
+  if (!dense) return fail(RSQ_E_INVALID, "dense is NULL");
+  if (!rsq::aligned(dense, 16)) return fail(RSQ_E_INVALID, "dense is not 16-byte aligned");
+  // it sets the host handle's counters, which a replayed graph would not
+  if (const rsq_status cs = refuse_capture(stream, "a state load")) return cs;
+  const int tiles = st->cfg.batch * st->cfg.heads;
+  const int64_t bytes = (int64_t)tiles * st->cfg.d_k * st->cfg.d_v * 4;
+  if (rsq::overlap({dense, bytes, "dense"}, {st->buf, (int64_t)st->layout.total, "state"}))
+    return fail(RSQ_E_INVALID, "dense overlaps the state's buffer");
+  const bool yoked = st->cfg.scale_mode == RSQ_SCALE_YOKED && !st->all32;
+  const rsq_status s = rsq::launch_state_load(base_args(st), tiles, dense, st->all32, yoked, stream);
+  if (s != RSQ_OK) return s;
+  st->t = 0;
+  st->n = 0;
+  return RSQ_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// workspace of a selective step: q, k, v, alpha and o of every tile, 256-byte aligned
+struct SsmWork {
+  size_t q, k, v, alpha, o, total;
+};
+
+SsmWork ssm_work(const rsq_state* st) {
+  const size_t tiles = (size_t)st->cfg.batch * st->cfg.heads, e = st->cfg.in_dtype == RSQ_BF16 ? 2 : 4;
+  SsmWork w;
+  w.q = 0;
+  w.k = w.q + align_up(tiles * st->cfg.d_k * e);
+  w.v = w.k + align_up(tiles * st->cfg.d_k * e);
+  w.alpha = w.v + align_up(tiles * st->cfg.d_v * e);
+  w.o = w.alpha + align_up(tiles * 4);
+  w.total = w.o + align_up(tiles * st->cfg.d_v * 4);
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+rsq_status rsq_decode_ssm_workspace(const rsq_state* st, size_t* bytes) {
+  if (!st || !bytes) return fail(RSQ_E_INVALID, "NULL argument");
+  *bytes = ssm_work(st).total;
+  return RSQ_OK;
+}
+
+rsq_status rsq_decode_ssm_step(rsq_state* st, const rsq_ssm* p, void* stream) {
+  if (!st) return fail(RSQ_E_INVALID, "state is NULL");
+  if (const rsq_status s = rsq::check_ssm(p, false)) return s;
+  if (st->cfg.model != RSQ_MAMBA2) return fail(RSQ_E_INVALID, "a selective step needs a Mamba2 state");
+  if (p->state) return fail(RSQ_E_INVALID, "the step's state is the handle's: ssm.state must be NULL");
+  if (p->dtype != st->cfg.in_dtype || p->seqs != st->cfg.batch || p->heads != st->cfg.heads ||
+      p->d_k != st->cfg.d_k || p->d_v != st->cfg.d_v)
+    return fail(RSQ_E_INVALID, "dtype, seqs, heads, d_k and d_v must be the state's");
+  if (const rsq_status s = rsq::check_ssm_memory(p)) return s;
+  const SsmWork w = ssm_work(st);
+  if (!p->workspace || !rsq::aligned(p->workspace, 256))
+    return fail(RSQ_E_INVALID, "workspace is NULL or not 256-byte aligned");
+  if (p->workspace_bytes < w.total)
+    return fail(RSQ_E_BUFFER, "workspace has %zu bytes, the step needs %zu", p->workspace_bytes, w.total);
+  const int size = p->dtype == RSQ_BF16 ? 2 : 4;
+  const rsq::Span buf{st->buf, (int64_t)st->layout.total, "state"};
+  const rsq::Span y{p->y, rsq::span_bytes(p->tokens, p->y_stride, (int64_t)p->heads * p->d_v, size), "y"};
+  if (rsq::overlap(buf, y) || rsq::overlap(buf, {p->workspace, (int64_t)p->workspace_bytes, "workspace"}))
+    return fail(RSQ_E_INVALID, "y or workspace overlaps the state's buffer");
+  if (st->bypass && st->n >= st->cap)
+    return fail(RSQ_E_BYPASS_FULL, "bypass holds %d of %d columns: call rsq_merge_bypass", st->n, st->cap);
+  if (st->bypass) {
+    if (const rsq_status cs = refuse_capture(stream, "a decode step of a state with a bypass")) return cs;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+  const rsq::SsmArgs a = rsq::ssm_args(p);
+  const rsq::SsmGates g{ws + w.q, ws + w.k, ws + w.v, reinterpret_cast<float*>(ws + w.alpha)};
+  float* o = reinterpret_cast<float*>(ws + w.o);
+  const bool bf16 = p->dtype == RSQ_BF16;
+  if (const rsq_status s = rsq::launch_ssm_gates(a, bf16, g, stream)) return s;
+  if (const rsq_status s = rsq_decode_step(st, g.q, g.k, g.v, g.alpha, nullptr, o, stream)) return s;
+  return rsq::launch_ssm_skip(a, bf16, o, stream);
 }
 
 rsq_status rsq_get_status(rsq_state* st, uint32_t* flags, void* stream) {

@@ -48,4 +48,16 @@ rsq_status check_ssm(const rsq_ssm* p, bool prompt);
 rsq_status check_ssm_memory(const rsq_ssm* p);
 SsmArgs ssm_args(const rsq_ssm* p);
 
+// The decode step's inputs of one token: q and k from the head's C and B, v =
+// delta x rounded to the inputs' type, alpha = exp(delta A).
+struct SsmGates {
+  void* q;
+  void* k;
+  void* v;
+  float* alpha;
+};
+rsq_status launch_ssm_gates(const SsmArgs& a, bool bf16, const SsmGates& out, void* stream);
+// y = o + D x
+rsq_status launch_ssm_skip(const SsmArgs& a, bool bf16, const float* o, void* stream);
+
 }  // namespace rsq

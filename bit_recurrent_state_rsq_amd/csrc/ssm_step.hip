@@ -144,7 +144,55 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
   }
 }
 
+// Inputs of a decode step on a quantized state: a workgroup per head and
+// sequence. They are d_k + d_v elements a head against the d_k d_v of the state
+// that the step then moves.
+template <typename T>
+__global__ __launch_bounds__(128) void ssm_gates_kernel(SsmArgs a, SsmGates o) {
+  const int64_t tile = blockIdx.x;
+  const int h = (int)(tile % a.H);
+  const int64_t s = tile / a.H;
+  const int group = h / a.per_group;
+  const float d = ssm_delta<T>(a, s, h);
+  if (threadIdx.x == 0) o.alpha[tile] = expf(d * a.A[h]);
+  const T* x = reinterpret_cast<const T*>(a.x) + s * a.x_stride + (int64_t)h * a.dv;
+  const T* B = reinterpret_cast<const T*>(a.B) + s * a.b_stride + (int64_t)group * a.dk;
+  const T* C = reinterpret_cast<const T*>(a.C) + s * a.c_stride + (int64_t)group * a.dk;
+  for (int i = threadIdx.x; i < a.dk; i += 128) {
+    reinterpret_cast<T*>(o.q)[tile * a.dk + i] = C[i];
+    reinterpret_cast<T*>(o.k)[tile * a.dk + i] = B[i];
+  }
+  for (int j = threadIdx.x; j < a.dv; j += 128) from_f32(d * to_f32(x[j]), reinterpret_cast<T*>(o.v)[tile * a.dv + j]);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void ssm_skip_kernel(SsmArgs a, const float* o) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t hv = (int64_t)a.H * a.dv;
+  const int64_t s = id / hv;
+  if (s >= a.q.seqs) return;
+  const int64_t j = id - s * hv;
+  float y = o[id];
+  if (a.D) y = __builtin_fmaf(a.D[j / a.dv], to_f32(reinterpret_cast<const T*>(a.x)[s * a.x_stride + j]), y);
+  from_f32(y, reinterpret_cast<T*>(a.y)[s * a.y_stride + j]);
+}
+
 }  // namespace
+
+rsq_status launch_ssm_gates(const SsmArgs& a, bool bf16, const SsmGates& out, void* stream) {
+  const unsigned tiles = (unsigned)((int64_t)a.q.seqs * a.H);
+  if (bf16) hipLaunchKernelGGL(ssm_gates_kernel<Bf16>, dim3(tiles), dim3(128), 0, (hipStream_t)stream, a, out);
+  else hipLaunchKernelGGL(ssm_gates_kernel<float>, dim3(tiles), dim3(128), 0, (hipStream_t)stream, a, out);
+  return launched("step gates");
+}
+
+rsq_status launch_ssm_skip(const SsmArgs& a, bool bf16, const float* o, void* stream) {
+  const unsigned blocks = (unsigned)ceil_div((int64_t)a.q.seqs * a.H * a.dv, 256);
+  if (bf16) hipLaunchKernelGGL(ssm_skip_kernel<Bf16>, dim3(blocks), dim3(256), 0, (hipStream_t)stream, a, o);
+  else hipLaunchKernelGGL(ssm_skip_kernel<float>, dim3(blocks), dim3(256), 0, (hipStream_t)stream, a, o);
+  return launched("step skip connection");
+}
+
 }  // namespace rsq
 
 using namespace rsq;

@@ -36,7 +36,7 @@ def _torch():
 _DTYPE = {}   # activation types, filled with torch
 
 
-class _On:
+class On:
     """The device and stream of a call: tensors made inside belong to both."""
 
     def __init__(self, device, stream):
@@ -154,7 +154,7 @@ def _conv(x, seqs, tokens, max_len, offsets, weight, bias, state, activation, ou
               and tuple(state.shape) == (seqs, C, W - 1), "state must be a contiguous %s tensor of shape %s on %s, got %s %s",
               x.dtype, (seqs, C, W - 1), x.device, state.dtype, tuple(state.shape))
         c.state = state.data_ptr()
-    with _On(x.device, stream) as on:
+    with On(x.device, stream) as on:
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         _, c.y_stride = _rows(out, x, (C,), "out", x.shape[:-1])
@@ -222,7 +222,7 @@ def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, softplus=False, state=None, o
     need = ctypes.c_size_t()
     p.y_stride = p.x_stride
     p.state_in = int(state is not None)
-    with _On(x.device, stream) as on:
+    with On(x.device, stream) as on:
         if state is None:
             state = torch.empty(shape, dtype=torch.float32, device=x.device)
         p.state = _param(state, x.device, shape, "state")
@@ -250,12 +250,33 @@ def ssm_step(state, x, dt, A, B, C, D=None, dt_bias=None, softplus=False, out=No
     _need(state is not None, "state is required")
     p.state = _param(state, x.device, (n, p.heads, p.d_k, p.d_v), "state")
     p.state_in = 1
-    with _On(x.device, stream) as on:
+    with On(x.device, stream) as on:
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         _, p.y_stride = _rows(out, x, (p.heads, p.d_v), "out", x.shape[:-2])
         p.y = out.data_ptr()
         check(lib.rsq_ssm_step(ctypes.byref(p), on.ptr))
+    return out
+
+
+def state_ssm_step(st, x, dt, A, B, C, D, dt_bias, softplus, out, stream):
+    """State.ssm_step."""
+    torch = _torch()
+    _need(x.dim() == 3 and B.dim() == 3, "x and B must have shape [batch, heads, d_v] and [batch, groups, d_k]")
+    _need(x.device == st.device, "x must be on %s", st.device)
+    n = x.shape[0]
+    p = _ssm(x, dt, A, B, C, D, dt_bias, softplus, n, n, 1, None)
+    need = ctypes.c_size_t()
+    check(lib.rsq_decode_ssm_workspace(st.h, ctypes.byref(need)))
+    with On(x.device, stream) as on:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _, p.y_stride = _rows(out, x, (p.heads, p.d_v), "out", x.shape[:-2])
+        p.y = out.data_ptr()
+        # torch's allocations are 512-byte aligned; the call's stream owns this one
+        work = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+        p.workspace, p.workspace_bytes = work.data_ptr(), need.value
+        check(lib.rsq_decode_ssm_step(st.h, ctypes.byref(p), on.ptr))
     return out
 
 
@@ -290,7 +311,7 @@ def rms_norm(x, weight, eps=1e-5, residual=None, out_dtype=None, group=0, out=No
         _, p.residual_stride = _rows(residual, x, (cols,), "residual", x.shape[:-1])
         p.residual = residual.data_ptr()
     groups = cols // p.group if p.group > 0 else 1
-    with _On(x.device, stream) as on:
+    with On(x.device, stream) as on:
         if out is None:
             out = torch.empty(x.shape, dtype=torch_out, device=x.device)
         _need(out.dtype == torch_out, "out must be %s, got %s", torch_out, out.dtype)
@@ -327,7 +348,7 @@ class W4Weight:
         self.device = codes.device
         need = ctypes.c_size_t()
         check(lib.rsq_w4_bytes(self.n, self.k, self.group, self.scale_dtype, ctypes.byref(need)))
-        with _On(codes.device, stream) as on:
+        with On(codes.device, stream) as on:
             self.packed = torch.empty(need.value, dtype=torch.uint8, device=codes.device)
             check(lib.rsq_w4_pack(codes.data_ptr(), scales.data_ptr(), self.n, self.k, self.group, self.scale_dtype,
                                   self.packed.data_ptr(), need.value, on.ptr))
@@ -363,7 +384,7 @@ def w4_linear(x, weight, x_scale=None, out_dtype=None, out=None, stream=None):
         out_dtype = "f32" if x.dtype == torch.float32 else "bf16"
     _need(out_dtype in outs, "out_dtype must be 'f32' or 'bf16', got %r", out_dtype)
     p.out_dtype, torch_out = outs[out_dtype]
-    with _On(x.device, stream) as on:
+    with On(x.device, stream) as on:
         if out is None:
             out = torch.empty(lead + (weight.n,), dtype=torch_out, device=x.device)
         _need(out.dtype == torch_out and out.device == x.device, "out must be %s on %s", torch_out, x.device)

@@ -411,6 +411,25 @@ rsq_status rsq_ssm_scan(const rsq_ssm* ssm, void* stream);
 rsq_status rsq_ssm_step(const rsq_ssm* ssm, void* stream);
 
 /*
+ * The same single-token step on a quantized state (model RSQ_MAMBA2; dtype,
+ * seqs, heads, d_k and d_v as configured; ssm->state NULL): the gates, then
+ * rsq_decode_step with q = C, k = B, v = delta x (rounded to dtype) and alpha =
+ * exp(delta A), then y = o + D x. The workspace is 256-byte aligned. Capture
+ * and a full bypass as in rsq_decode_step.
+ */
+rsq_status rsq_decode_ssm_workspace(const rsq_state* st, size_t* bytes);
+rsq_status rsq_decode_ssm_step(rsq_state* st, const rsq_ssm* ssm, void* stream);
+
+/*
+ * Put a dense fp32 state (device [batch][heads][d_k][d_v], 16-byte aligned,
+ * such as a scan's) into a state of any model, as its first one: every group's
+ * step is absmax / qmax, the codes are rounded to nearest-even, a yoked
+ * reference takes the dense values, the bypass or the window is empty and the
+ * step count 0. RSQ_E_UNSUPPORTED while `stream` is capturing.
+ */
+rsq_status rsq_state_load(rsq_state* st, const float* dense, void* stream);
+
+/*
  * Root-mean-square norm of rows:
  *   h = x + residual (stored back to residual, rounded to dtype; residual NULL: h = x)
  *   y = h / sqrt(mean(h^2) + eps) * weight, of the fp32 h
