@@ -258,8 +258,8 @@ class State:
         if dense is None:
             raise ValueError("dense is required")
         p = self._ptr(dense, torch.float32, shape, "dense")
-        with _layer.On(self.device, stream) as on:
-            check(lib.rsq_state_load(self.h, p, on.ptr))
+        with _layer.on(dense.get_device(), stream) as s:
+            check(lib.rsq_state_load(self.h, p, s))
 
     def ssm_step(self, x, dt, A, B, C, D=None, dt_bias=None, softplus=False, out=None, stream=None):
         """One token of a Mamba2 layer on this state (rsq_decode_ssm_step): the arguments of the

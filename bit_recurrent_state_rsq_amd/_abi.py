@@ -131,17 +131,18 @@ def _load():
         "rsq_abi_version": (I32, []),
         "rsq_allocate_head_bits": (I32, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float), I32,
                                          ctypes.c_float, ctypes.POINTER(I32)]),
-        "rsq_causal_conv": (I32, [ctypes.POINTER(Conv), P]),
-        "rsq_ssm_scan_workspace": (I32, [ctypes.POINTER(Ssm), ctypes.POINTER(SZ)]),
-        "rsq_ssm_scan": (I32, [ctypes.POINTER(Ssm), P]),
-        "rsq_ssm_step": (I32, [ctypes.POINTER(Ssm), P]),
-        "rsq_rms_norm": (I32, [ctypes.POINTER(Norm), P]),
+        # struct arguments as addresses: the callers pass a packed struct's bytes
+        "rsq_causal_conv": (I32, [P, P]),
+        "rsq_ssm_scan_workspace": (I32, [P, ctypes.POINTER(SZ)]),
+        "rsq_ssm_scan": (I32, [P, P]),
+        "rsq_ssm_step": (I32, [P, P]),
+        "rsq_rms_norm": (I32, [P, P]),
         "rsq_w4_bytes": (I32, [I32, I32, I32, I32, ctypes.POINTER(SZ)]),
         "rsq_w4_pack": (I32, [P, P, I32, I32, I32, I32, P, SZ, P]),
-        "rsq_w4_linear": (I32, [ctypes.POINTER(W4), P]),
+        "rsq_w4_linear": (I32, [P, P]),
         "rsq_state_load": (I32, [P, P, P]),
         "rsq_decode_ssm_workspace": (I32, [P, ctypes.POINTER(SZ)]),
-        "rsq_decode_ssm_step": (I32, [P, ctypes.POINTER(Ssm), P]),
+        "rsq_decode_ssm_step": (I32, [P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
