@@ -5,6 +5,8 @@
 //   P_ts = e^{c_t - c_s} d_s (C_t . B_s),
 //   S   <- e^{c_L} S0 + sum_s B_s (d_s e^{c_L - c_s} x_s)^T:
 // four small matrix products a chunk, on the matrix cores.
+#include <initializer_list>
+
 #include "host_util.hpp"
 #include "ssm.hpp"
 
@@ -20,7 +22,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kL = 64;        // tokens of a chunk
 constexpr int kV = 64;        // state columns of a workgroup
 constexpr int kThreads = 256;
-constexpr int kPad = 8;       // elements behind each LDS row: rows start 16 bytes apart in the banks
 
 struct ScanArgs {
   SsmArgs s;
@@ -58,17 +59,34 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[N]) {
   }
 }
 
+// A chunk's rows as a buffer: one scalar base, 32-bit offsets, and rows past the
+// sequence's end out of its range, where loads give zeros and stores are dropped.
+// Offsets of lanes without a row or column of their own start at kOutside.
+constexpr uint32_t kOutside = 0x80000000u;
+constexpr int64_t kMaxRowBytes = 1 << 24;   // a chunk then ends below 2^30, and nothing wraps
+struct Rows {
+  __amdgpu_buffer_rsrc_t rsrc;
+  __device__ __forceinline__ Rows(const void* base, int64_t row_bytes, int t0, int len) {
+    // uniform over the workgroup
+    const uint64_t p = reinterpret_cast<uint64_t>(base) + (uint64_t)(t0 * row_bytes);
+    // (the builtin's int goes through uint32_t: it must not extend its sign)
+    const uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+    const uint32_t high = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
+    const uint64_t u = (uint64_t)high << 32 | low;
+    const int rows = min(max(len - t0, 0), kL);
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0,
+                                             __builtin_amdgcn_readfirstlane((int)(rows * row_bytes)), 0x00020000);
+  }
+};
+
 // 8 consecutive input elements as PI pieces of 4 words each
 template <typename T, int PI>
 struct Vec8 {
   u32x4 raw[PI == 1 ? 1 : 2];
-  __device__ __forceinline__ void zero() {
+  __device__ __forceinline__ void load(const Rows& r, uint32_t offset) {
 #pragma unroll
-    for (auto& r : raw) r = u32x4{0u, 0u, 0u, 0u};
-  }
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < (PI == 1 ? 1 : 2); ++i) raw[i] = reinterpret_cast<const u32x4*>(p)[i];
+    for (int i = 0; i < (PI == 1 ? 1 : 2); ++i)
+      raw[i] = __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, (int)(offset + 16 * i), 0, 0);
   }
   __device__ __forceinline__ void pieces(u32x4 (&out)[PI]) const {
     if constexpr (PI == 1) {
@@ -92,56 +110,96 @@ struct Vec8 {
     if constexpr (PI == 1) raw[0][e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
     else raw[e >> 2][e & 3] = 0u;
   }
+  // an exponent of all ones carries into the sign's place when one is added
   __device__ __forceinline__ bool any_bad() const {
-    bool b = false;
+    uint32_t t = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) b = b || bad(e);
-    return b;
+    for (const auto& r : raw)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        t |= PI == 1 ? (r[i] & 0x7F807F80u) + 0x00800080u : (r[i] & 0x7F800000u) + 0x00800000u;
+    return (t & (PI == 1 ? 0x80008000u : 0x80000000u)) != 0u;
   }
 };
 
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// Transposed read: rows r0 .. r0 + 3 of 16 columns from c0 on, where r0 is the
-// 16-lane group's; lane i of the group gets the four rows' elements of column
-// c0 + i. (ds_read_b64_tr_b16: lane i names the i-th run of four elements.)
-__device__ __forceinline__ u32x2 read_tr(const uint16_t* base, int stride, int r0, int c0, int lane) {
-  const int i = lane & 15;
-  const uint16_t* p = base + (r0 + (i >> 2)) * stride + c0 + 4 * (i & 3);
+// A tile in LDS: rows of 2^n 16-byte pieces, none padded. Piece p of row r sits
+// at p ^ f(r) of its row, with f such that 16 consecutive rows' pieces p are in
+// 16 different groups of four banks (reads of a fragment's rows), and eight
+// rows' pairs (2 p, 2 p + 1) in eight different pairs of groups (transposed
+// reads). Rows of 128 bytes share the banks with their neighbour, so f then
+// follows from the other bits. f goes by the row modulo 16 only, and pieces are
+// joined by exclusive or: a lane has one address for each kind of access, and
+// reaches other rows by adding multiples of 16 of them and other pieces by an
+// exclusive or with a constant.
+template <int ROW>   // elements of a row
+struct Tile {
+  static constexpr int kBytes = 2 * ROW;
+  static __device__ __forceinline__ uint32_t at(int row, int piece) {
+    const int f = ROW >= 128 ? ((row << 1) | ((row >> 3) & 1)) & 15 : ((row & 6) | ((row >> 3) & 1));
+    return (uint32_t)(row * kBytes + ((piece ^ f) << 4));
+  }
+  // a fragment's piece of row lane % 16: pieces 4 i + lane / 16 (exclusive or 64 i)
+  static __device__ __forceinline__ uint32_t fragment(int lane) { return at(lane & 15, lane >> 4); }
+  // four elements 4 (lane / 16) of 16 columns of a row (exclusive or 32 a further 16 columns)
+  static __device__ __forceinline__ uint32_t four(int row, int lane) {
+    return at(row, lane >> 5) + 8 * ((lane >> 4) & 1);
+  }
+  // Transposed reads (ds_read_b64_tr_b16: in a group of 16 lanes, lane i names
+  // the i-th run of four elements and gets the i-th column): lane group g takes
+  // rows 4 g .. 4 g + 3 of 16 columns (exclusive or 32 a further 16 columns).
+  static __device__ __forceinline__ uint32_t transposed(int lane) {
+    const int i = lane & 15;
+    return at(4 * (lane >> 4) + (i >> 2), (i >> 1) & 1) + 8 * (i & 1);
+  }
+};
+
+__device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
 }
 
 // Contraction index of a k-step of 32 over tokens: lane group g holds tokens
 // 4g .. 4g + 3 and 16 + 4g .. 16 + 4g + 3. A product's lanes hold its rows in
 // fours like this, so P leaves one product and enters the next in registers.
-__device__ __forceinline__ u32x4 read_tr8(const uint16_t* base, int stride, int r0, int c0, int lane) {
-  const int g = lane >> 4;
-  const u32x2 lo = read_tr(base, stride, r0 + 4 * g, c0, lane);
-  const u32x2 hi = read_tr(base, stride, r0 + 16 + 4 * g, c0, lane);
+template <int ROW>
+__device__ __forceinline__ u32x4 read_tr8(const uint8_t* p) {
+  const u32x2 lo = read_tr(p), hi = read_tr(p + 16 * Tile<ROW>::kBytes);
   return u32x4{lo[0], lo[1], hi[0], hi[1]};
 }
+
+// Keeps what is derived from v inside the loop that this stands in: a register
+// each for dozens of addresses costs more than the operation that makes them.
+__device__ __forceinline__ void local(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
 // PI pieces of the inputs, PY of the computed factors of y (P and S), 3 of the
 // weighted x that enters the state (a state stays exact to fp32). Products of
 // pieces below 2^-24 are left out.
 //
-// Shares of the four wavefronts: for y, wavefront w owns the 16 tokens 16 w;
-// for the state, the 16 columns 16 w and all of d_k, in registers over the
-// whole segment. STATES: only the state is wanted (a segment before the last,
-// scanned first so that the segments can run side by side).
+// Shares of the four wavefronts: for y, wavefront w owns the 16 tokens 16 w (so
+// w + 1 tiles of P); for the state, the 16 columns 16 w and all of d_k, in
+// registers over the whole segment. Wavefront 0, with the fewest tiles of P,
+// works out the next chunk's decays. STATES: only the state is wanted (a
+// segment before the last, scanned first so that the segments can run side by
+// side).
 template <typename T, int DK, int PI, int PY, bool STATES>
-__global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_kernel(ScanArgs a) {
   constexpr int PW = 3;
   constexpr int KT = DK / 16, KS = DK / 32;
-  constexpr int SK = DK + kPad, SV = kV + kPad;
-  __shared__ __attribute__((aligned(16))) uint16_t lds_b[PI][kL][SK];
-  __shared__ __attribute__((aligned(16))) uint16_t lds_x[PI][kL][SV];
-  __shared__ __attribute__((aligned(16))) uint16_t lds_s[STATES ? 1 : PY][STATES ? 1 : kV][SK];   // S^T: [column][key]
-  __shared__ __attribute__((aligned(16))) float lds_hi[kL], lds_lo[kL], lds_d[kL], lds_w[kL];
+  typedef Tile<DK> TB;
+  typedef Tile<kV> TX;
+  constexpr int BB = kL * TB::kBytes, XB = kL * TX::kBytes, SB = kV * TB::kBytes;   // bytes of a piece's tile
+  __shared__ __attribute__((aligned(16))) uint8_t lds_b[PI * BB];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_x[PI * XB];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_s[STATES ? 16 : PY * SB];   // S^T: [column][key]
+  // of a chunk's tokens, by the chunk's parity: c_t as a float pair, d_t, and d_t e^{c_L - c_t}
+  __shared__ __attribute__((aligned(16))) float lds_hi[2][kL], lds_lo[2][kL], lds_d[2][kL], lds_w[2][kL];
+  __shared__ float lds_decay[2];     // e^{c_L}
   __shared__ int lds_first[2][kV];   // first token of a column whose x is not finite
   __shared__ int lds_bad[2];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, g = lane >> 4;
   int id = blockIdx.x;
   const int h = id % a.s.H;
@@ -150,11 +208,12 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_ker
   id /= a.vblocks;
   const int seg = id % a.segs;
   const int sq = id / a.segs;
-  int64_t len;
-  const int64_t begin = seq_range(a.s.q, sq, len);
+  int64_t len64;
+  const int64_t begin = seq_range(a.s.q, sq, len64);
+  const int len = (int)len64;   // rows are counted in 31 bits
   const int dk = a.s.dk, dv = a.s.dv, v0 = vb * kV;
-  const int64_t chunks = (len + kL - 1) / kL;
-  const int used = (int)((chunks + a.seg_chunks - 1) / a.seg_chunks);
+  const int chunks = (int)((len64 + kL - 1) / kL);
+  const int used = (chunks + a.seg_chunks - 1) / a.seg_chunks;
   // the first pass covers the segments before the last; the second all of them
   if (STATES ? seg >= used - 1 : seg >= used && (seg > 0 || a.s.state_in)) return;
 
@@ -203,64 +262,96 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_ker
   const T* Bp = reinterpret_cast<const T*>(a.s.B) + begin * a.s.b_stride + (size_t)(h / a.s.per_group) * dk;
   const T* Cp = reinterpret_cast<const T*>(a.s.C) + begin * a.s.c_stride + (size_t)(h / a.s.per_group) * dk;
   T* y = reinterpret_cast<T*>(a.s.y) + begin * a.s.y_stride + (size_t)h * dv + v0;
+  const int xrow = (int)(a.s.x_stride * sizeof(T)), brow = (int)(a.s.b_stride * sizeof(T));
+  const int crow = (int)(a.s.c_stride * sizeof(T)), yrow = (int)(a.s.y_stride * sizeof(T));
   const float A2 = a.s.A[h] * 1.44269504088896f;   // decays in powers of two
   const float Dh = a.s.D ? a.s.D[h] : 0.f;
 
-  // ---- a chunk's rows, loaded one chunk ahead
-  constexpr int NB = kL * (DK / 8) / kThreads;
-  constexpr int NX = kL * (kV / 8) / kThreads;
-  Vec8<T, PI> rb[NB], rx[NX], rc[KS];
-  float delta = 0.f;
-  auto load = [&](int64_t t0) {
+  // ---- a chunk's rows: B and x go through registers to LDS one chunk ahead,
+  // C's rows 16 wave .. are fragments as they are
+  constexpr int NB = kL * (DK / 8) / kThreads, RB = kThreads / (DK / 8);   // loads a thread, rows of one load
+  constexpr int NX = kL * (kV / 8) / kThreads, RX = kThreads / (kV / 8);
+  Vec8<T, PI> rb[NB], rx[NX], rc[STATES ? 1 : KS];
+  const int bk = (tid % (DK / 8)) * 8, xv8 = (tid % (kV / 8)) * 8;
+  uint32_t boff = bk < dk ? (uint32_t)(tid / (DK / 8) * brow + bk * (int)sizeof(T)) : kOutside;
+  uint32_t xoff = v0 + xv8 < dv ? (uint32_t)(tid / (kV / 8) * xrow + xv8 * (int)sizeof(T)) : kOutside;
+  auto load_bx = [&](int t0) {
+    const Rows rB(Bp, brow, t0, len), rX(x, xrow, t0, len);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int u = tid + kThreads * i, k = (u % (DK / 8)) * 8;
-      const int64_t t = t0 + u / (DK / 8);
-      rb[i].zero();
-      if (t < len && k < dk) rb[i].load(Bp + t * a.s.b_stride + k);
-    }
+    for (int i = 0; i < NB; ++i) rb[i].load(rB, boff + (uint32_t)(i * RB * brow));
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const int u = tid + kThreads * i, v = (u % (kV / 8)) * 8;
-      const int64_t t = t0 + u / (kV / 8);
-      rx[i].zero();
-      if (t < len && v0 + v < dv) rx[i].load(x + t * a.s.x_stride + v);
-    }
-    if constexpr (!STATES) {
-      const int64_t t = t0 + 16 * wave + n16;
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const int k = 32 * i + 8 * g;
-        rc[i].zero();
-        if (t < len && k < dk) rc[i].load(Cp + t * a.s.c_stride + k);
-      }
-    }
-    // a row past the sequence neither decays nor adds
-    delta = t0 + lane < len ? ssm_delta<T>(a.s, begin + t0 + lane, h) : 0.f;
+    for (int i = 0; i < NX; ++i) rx[i].load(rX, xoff + (uint32_t)(i * RX * xrow));
   };
-
-  const int64_t c_end = chunks < (int64_t)(seg + 1) * a.seg_chunks ? chunks : (int64_t)(seg + 1) * a.seg_chunks;
-  int64_t c = (int64_t)seg * a.seg_chunks;
+  uint32_t coff = (uint32_t)((16 * wave + n16) * crow + 8 * g * (int)sizeof(T));
+  auto load_c = [&](int t0) {
+    const Rows rC(Cp, crow, t0, len);
+#pragma unroll
+    for (int i = 0; i < (STATES ? 0 : KS); ++i) {
+      uint32_t at = coff + (uint32_t)(32 * i * sizeof(T));
+      if (dk < DK) at = 32 * i + 8 * g < dk ? at : kOutside;
+      rc[i].load(rC, at);
+    }
+  };
+  // a load of fewer than 16 rows (d_k = 256: 8) moves f by the bit of row 8
+  auto flip = [](int rows) { return (uint32_t)((DK >= 128 ? (rows >> 3) & 1 : 0) << 4); };
+  uint32_t yoff = (uint32_t)((16 * wave + n16) * yrow + 4 * g * (int)sizeof(T));
+  // LDS addresses of this lane
+  uint32_t a_bput = TB::at(tid / (DK / 8), tid % (DK / 8)), a_xput = TX::at(tid / (kV / 8), tid % (kV / 8));
+  uint32_t a_frag = TB::fragment(lane), a_btr = TB::transposed(lane), a_xtr = TX::transposed(lane);
+  uint32_t a_sput = TB::four(16 * wave + n16, lane), a_xown = TX::four(16 * wave + n16, lane);
+  // Running sums of the log2 decays, in 64 bits: differences of them are small
+  // next to the sums where decays are strong. A row past the sequence neither
+  // decays nor adds.
   double total = 0.0;
-  if (c < c_end) load(c * kL);
+  auto decays = [&](float dt, int t0, int par) {
+    float delta = 0.f;
+    if (t0 + lane < len) {
+      delta = a.s.dt_bias ? dt + a.s.dt_bias[h] : dt;
+      if (a.s.softplus) delta = softplus(delta);
+    }
+    double cum = (double)delta * (double)A2;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const double o = __shfl_up(cum, m, 64);
+      if (lane >= m) cum += o;
+    }
+    const double last = __shfl(cum, 63, 64);
+    total += last;
+    const float hi = (float)cum;
+    lds_hi[par][lane] = hi;
+    lds_lo[par][lane] = (float)(cum - (double)hi);
+    lds_d[par][lane] = delta;
+    lds_w[par][lane] = __builtin_amdgcn_exp2f((float)(last - cum)) * delta;
+    if (lane == 0) lds_decay[par] = __builtin_amdgcn_exp2f((float)last);
+  };
+  const T* dtp = reinterpret_cast<const T*>(a.s.dt) + begin * a.s.dt_stride + h;
+  auto load_dt = [&](int t0) { return t0 + lane < len ? to_f32(dtp[(int64_t)(t0 + lane) * a.s.dt_stride]) : 0.f; };
+
+  const int c_end = min(chunks, (seg + 1) * a.seg_chunks);
+  int c = seg * a.seg_chunks;
+  if (c < c_end) {
+    load_bx(c * kL);
+    load_c(c * kL);
+    if (wave == 0) decays(load_dt(c * kL), c * kL, c & 1);
+  }
   if (tid < 2 * kV) lds_first[tid / kV][tid % kV] = kL;
   if (tid < 2) lds_bad[tid] = 0;
   __syncthreads();
   for (; c < c_end; ++c) {
-    const int64_t t0 = c * kL;
-    const int par = (int)(c & 1);
-    // ---- stage: inputs and the state to LDS, the decays
+    const int t0 = c * kL;
+    const int par = c & 1;
+    local(boff), local(xoff), local(coff), local(yoff), local(a_bput), local(a_xput), local(a_frag), local(a_btr);
+    local(a_xtr), local(a_sput), local(a_xown);
+    // ---- stage: inputs and the state to LDS
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int u = tid + kThreads * i;
       u32x4 p[PI];
       rb[i].pieces(p);
 #pragma unroll
-      for (int q = 0; q < PI; ++q) *reinterpret_cast<u32x4*>(&lds_b[q][u / (DK / 8)][(u % (DK / 8)) * 8]) = p[q];
+      for (int q = 0; q < PI; ++q) *reinterpret_cast<u32x4*>(lds_b + q * BB + i * RB * TB::kBytes + (a_bput ^ flip(i * RB))) = p[q];
     }
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-      const int u = tid + kThreads * i, row = u / (kV / 8), v = (u % (kV / 8)) * 8;
       // A product with x_s takes every s of a chunk, weights of later tokens
       // being zero: an infinity or a NaN there would reach earlier tokens. It
       // is taken out, and its column is NaN from its token on.
@@ -269,14 +360,14 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_ker
         for (int e = 0; e < 8; ++e)
           if (rx[i].bad(e)) {
             rx[i].clear(e);
-            atomicMin(&lds_first[par][v + e], row);
+            atomicMin(&lds_first[par][xv8 + e], tid / (kV / 8) + i * RX);
           }
         lds_bad[par] = 1;
       }
       u32x4 p[PI];
       rx[i].pieces(p);
 #pragma unroll
-      for (int q = 0; q < PI; ++q) *reinterpret_cast<u32x4*>(&lds_x[q][row][v]) = p[q];
+      for (int q = 0; q < PI; ++q) *reinterpret_cast<u32x4*>(lds_x + q * XB + i * RX * TX::kBytes + a_xput) = p[q];
     }
     if constexpr (!STATES) {
 #pragma unroll
@@ -286,79 +377,64 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_ker
         split_pair<PY>(S[kt][2], S[kt][3], hi);
 #pragma unroll
         for (int q = 0; q < PY; ++q)
-          *reinterpret_cast<u32x2*>(&lds_s[q][16 * wave + n16][16 * kt + 4 * g]) = u32x2{lo[q], hi[q]};
+          *reinterpret_cast<u32x2*>(lds_s + q * SB + (a_sput ^ (kt << 5))) = u32x2{lo[q], hi[q]};
       }
     }
-    // running sums of the log2 decays, in 64 bits: differences of them are
-    // small next to the sums where decays are strong
-    double cum = (double)delta * (double)A2;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const double o = __shfl_up(cum, m, 64);
-      if (lane >= m) cum += o;
-    }
-    const double last = __shfl(cum, 63, 64);
-    const float decay = __builtin_amdgcn_exp2f((float)last);
-    total += last;
-    if (wave == 0) {
-      const float hi = (float)cum;
-      lds_hi[lane] = hi;
-      lds_lo[lane] = (float)(cum - (double)hi);
-      lds_d[lane] = delta;
-      lds_w[lane] = __builtin_amdgcn_exp2f((float)(last - cum)) * delta;
-    }
-    u32x4 cf[STATES ? 1 : KS][PI];
-    if constexpr (!STATES) {
-#pragma unroll
-      for (int i = 0; i < KS; ++i) rc[i].pieces(cf[i]);
-    }
     __syncthreads();
-    const bool bad = lds_bad[par] != 0;
-    if (c + 1 < c_end) load(t0 + kL);
+    const bool bad = __builtin_amdgcn_readfirstlane(lds_bad[par]) != 0;
+    const bool more = c + 1 < c_end;
+    float dt_next = 0.f;
+    if (more) {
+      load_bx(t0 + kL);
+      if (wave == 0) dt_next = load_dt(t0 + kL);
+    }
     if (tid < kV) lds_first[par ^ 1][tid] = kL;
     if (tid == kV) lds_bad[par ^ 1] = 0;
 
     if constexpr (!STATES) {
+      u32x4 cf[KS][PI];
+#pragma unroll
+      for (int i = 0; i < KS; ++i) rc[i].pieces(cf[i]);
       const int tt = 16 * wave + n16;   // this lane's token
-      const float chi = lds_hi[tt], clo = lds_lo[tt];
-      // ---- P^T (rows s, columns t), two tiles of s a k-step, up to the diagonal
-      u32x4 pf[2][PY];
+      const float chi = lds_hi[par][tt], clo = lds_lo[par][tt];
+      // ---- P^T (rows s, columns t), tile by tile up to the diagonal
+      u32x4 pf[kL / 32][PY];
 #pragma unroll
-      for (int st2 = 0; st2 < 2; ++st2) {
-        if (2 * st2 > wave) break;
+      for (int j = 0; j < kL / 16; ++j) {
+        uint32_t lo[PY], hi[PY];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int s0 = 32 * st2 + 16 * half;
+        for (int q = 0; q < PY; ++q) lo[q] = hi[q] = 0u;
+        if (j <= wave) {
           f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-          if (s0 <= 16 * wave) {
 #pragma unroll
-            for (int i = 0; i < KS; ++i)
+          for (int i = 0; i < KS; ++i)
 #pragma unroll
-              for (int p = 0; p < PI; ++p) {
-                const u32x4 bf = *reinterpret_cast<const u32x4*>(&lds_b[p][s0 + n16][32 * i + 8 * g]);
+            for (int p = 0; p < PI; ++p) {
+              const u32x4 bf = *reinterpret_cast<const u32x4*>(lds_b + p * BB + 16 * j * TB::kBytes + (a_frag ^ (i << 6)));
 #pragma unroll
-                for (int q = 0; q < PI; ++q)
-                  if (p + q < 3) acc = mfma(bf, cf[i][q], acc);
-              }
+              for (int q = 0; q < PI; ++q)
+                if (p + q < 3) acc = mfma(bf, cf[i][q], acc);
+            }
+          const f32x4 shi = *reinterpret_cast<const f32x4*>(&lds_hi[par][16 * j + 4 * g]);
+          const f32x4 slo = *reinterpret_cast<const f32x4*>(&lds_lo[par][16 * j + 4 * g]);
+          const f32x4 sd = *reinterpret_cast<const f32x4*>(&lds_d[par][16 * j + 4 * g]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[r] *= __builtin_amdgcn_exp2f((chi - shi[r]) + (clo - slo[r])) * sd[r];
+          if (j == wave) {   // later tokens: out, whatever their weight
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = 4 * g + r <= n16 ? acc[r] : 0.f;
           }
-          const f32x4 shi = *reinterpret_cast<const f32x4*>(&lds_hi[s0 + 4 * g]);
-          const f32x4 slo = *reinterpret_cast<const f32x4*>(&lds_lo[s0 + 4 * g]);
-          const f32x4 sd = *reinterpret_cast<const f32x4*>(&lds_d[s0 + 4 * g]);
-          float pv[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float e = __builtin_amdgcn_exp2f((chi - shi[r]) + (clo - slo[r]));
-            pv[r] = s0 + 4 * g + r <= tt ? acc[r] * (e * sd[r]) : 0.f;
-          }
-          uint32_t lo[PY], hi[PY];
-          split_pair<PY>(pv[0], pv[1], lo);
-          split_pair<PY>(pv[2], pv[3], hi);
-#pragma unroll
-          for (int q = 0; q < PY; ++q) pf[st2][q][2 * half] = lo[q], pf[st2][q][2 * half + 1] = hi[q];
+          split_pair<PY>(acc[0], acc[1], lo);
+          split_pair<PY>(acc[2], acc[3], hi);
         }
+#pragma unroll
+        for (int q = 0; q < PY; ++q) pf[j / 2][q][2 * (j & 1)] = lo[q], pf[j / 2][q][2 * (j & 1) + 1] = hi[q];
+        __builtin_amdgcn_sched_barrier(0);
       }
       // ---- y^T (rows v, columns t)
       const float et = __builtin_amdgcn_exp2f(chi + clo);
+      const Rows rY(y, yrow, t0, len);
 #pragma unroll
       for (int vt = 0; vt < kV / 16; ++vt) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -366,7 +442,7 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_ker
         for (int i = 0; i < KS; ++i)
 #pragma unroll
           for (int p = 0; p < PY; ++p) {
-            const u32x4 sf = *reinterpret_cast<const u32x4*>(&lds_s[p][16 * vt + n16][32 * i + 8 * g]);
+            const u32x4 sf = *reinterpret_cast<const u32x4*>(lds_s + p * SB + 16 * vt * TB::kBytes + (a_frag ^ (i << 6)));
 #pragma unroll
             for (int q = 0; q < PI; ++q)
               if (p + q < 3) acc = mfma(sf, cf[i][q], acc);
@@ -374,40 +450,46 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_ker
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[r] *= et;
 #pragma unroll
-        for (int st2 = 0; st2 < 2; ++st2) {
-          if (2 * st2 > wave) break;
+        for (int j2 = 0; j2 < kL / 32; ++j2) {
+          if (2 * j2 <= wave) {
 #pragma unroll
-          for (int p = 0; p < PI; ++p) {
-            const u32x4 xf = read_tr8(&lds_x[p][0][0], SV, 32 * st2, 16 * vt, lane);
+            for (int p = 0; p < PI; ++p) {
+              const u32x4 xf = read_tr8<kV>(lds_x + p * XB + 32 * j2 * TX::kBytes + (a_xtr ^ (vt << 5)));
 #pragma unroll
-            for (int q = 0; q < PY; ++q)
-              if (p + q < 3) acc = mfma(xf, pf[st2][q], acc);
+              for (int q = 0; q < PY; ++q)
+                if (p + q < 3) acc = mfma(xf, pf[j2][q], acc);
+            }
           }
         }
         // D x, from the pieces of x (their sum is exact)
         float xv[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = PI - 1; p >= 0; --p) {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(&lds_x[p][tt][16 * vt + 4 * g]);
+          const u32x2 w = *reinterpret_cast<const u32x2*>(lds_x + p * XB + (a_xown ^ (vt << 5)));
           xv[0] += __uint_as_float(w[0] << 16), xv[1] += __uint_as_float(w[0] & 0xFFFF0000u);
           xv[2] += __uint_as_float(w[1] << 16), xv[3] += __uint_as_float(w[1] & 0xFFFF0000u);
         }
         float out[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          out[r] = __builtin_fmaf(Dh, xv[r], acc[r]);
-          if (bad && tt >= lds_first[par][16 * vt + 4 * g + r]) out[r] = __builtin_nanf("");
+        for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], acc[r]);
+        if (bad) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (tt >= lds_first[par][16 * vt + 4 * g + r]) out[r] = __builtin_nanf("");
         }
-        const int v = 16 * vt + 4 * g;
-        if (t0 + tt < len && v0 + v < dv) {
-          T* yp = y + (t0 + tt) * a.s.y_stride + v;
-          if constexpr (PI == 1) *reinterpret_cast<u32x2*>(yp) = u32x2{bf16_pair(out[0], out[1]), bf16_pair(out[2], out[3])};
-          else *reinterpret_cast<f32x4*>(yp) = f32x4{out[0], out[1], out[2], out[3]};
-        }
+        uint32_t at = yoff + (uint32_t)(16 * vt * sizeof(T));
+        if (v0 + kV > dv) at = v0 + 16 * vt + 4 * g < dv ? at : kOutside;
+        if constexpr (PI == 1)
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(out[0], out[1]), bf16_pair(out[2], out[3])}, rY.rsrc, (int)at, 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{out[0], out[1], out[2], out[3]}), rY.rsrc, (int)at, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (more) load_c(t0 + kL);
     }
 
     // ---- S <- decay S + B^T (w x)
+    const float decay = lds_decay[par];
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -416,9 +498,9 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_ker
     for (int ts = 0; ts < kL / 32; ++ts) {
       u32x4 xr[PI];
 #pragma unroll
-      for (int p = 0; p < PI; ++p) xr[p] = read_tr8(&lds_x[p][0][0], SV, 32 * ts, 16 * wave, lane);
-      const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds_w[32 * ts + 4 * g]);
-      const f32x4 w1 = *reinterpret_cast<const f32x4*>(&lds_w[32 * ts + 16 + 4 * g]);
+      for (int p = 0; p < PI; ++p) xr[p] = read_tr8<kV>(lds_x + p * XB + 32 * ts * TX::kBytes + (a_xtr ^ (wave << 5)));
+      const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds_w[par][32 * ts + 4 * g]);
+      const f32x4 w1 = *reinterpret_cast<const f32x4*>(&lds_w[par][32 * ts + 16 + 4 * g]);
       u32x4 xw[PW];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -439,18 +521,28 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 2) void scan_ker
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int p = 0; p < PI; ++p) {
-          const u32x4 bf = read_tr8(&lds_b[p][0][0], SK, 32 * ts, 16 * kt, lane);
+          const u32x4 bf = read_tr8<DK>(lds_b + p * BB + 32 * ts * TB::kBytes + (a_btr ^ (kt << 5)));
 #pragma unroll
           for (int q = 0; q < PW; ++q)
             if (p + q < 3) S[kt] = mfma(bf, xw[q], S[kt]);
+          if (kt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if (bad && lds_first[par][16 * wave + n16] < kL) {
+    // A matrix product's result may be read by other instructions only some
+    // cycles after its issue. The compiler counts them out, but was seen not to
+    // across the branch below (with S in accumulation registers).
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15");
+    __builtin_amdgcn_sched_barrier(0);
+    if (bad) {
+      if (lds_first[par][16 * wave + n16] < kL) {
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[kt][r] = __builtin_nanf("");
+          for (int r = 0; r < 4; ++r) S[kt][r] = __builtin_nanf("");
+      }
     }
+    if (wave == 0 && more) decays(dt_next, t0 + kL, par ^ 1);
     __syncthreads();   // the chunk's LDS has been read
   }
 
@@ -497,10 +589,10 @@ struct ScanPlan {
 };
 
 // Sequences are cut into segments that run side by side when heads and
-// sequences alone do not fill the chip: about kTarget workgroups (two for each
+// sequences alone do not fill the chip: about kTarget workgroups (three for each
 // of 256 compute units) of equal length. Every segment but a sequence's last is
 // read twice (its state first), so one segment is kept where that fills it.
-constexpr int64_t kTarget = 512, kMinChunks = 4;
+constexpr int64_t kTarget = 768, kMinChunks = 4;
 
 rsq_status plan_scan(const rsq_ssm* p, ScanPlan& w) {
   w.dkp = p->d_k <= 64 ? 64 : p->d_k <= 128 ? 128 : 256;
@@ -542,6 +634,10 @@ extern "C" rsq_status rsq_ssm_scan(const rsq_ssm* p, void* stream) {
   if (const rsq_status s = check_ssm(p, true)) return s;
   if (!p->state) return fail(RSQ_E_INVALID, "state is NULL");
   if (const rsq_status s = check_ssm_memory(p)) return s;
+  const int64_t size = p->dtype == RSQ_BF16 ? 2 : 4;
+  for (const int64_t stride : {p->x_stride, p->b_stride, p->c_stride, p->y_stride})
+    if (stride * size > kMaxRowBytes)
+      return fail(RSQ_E_UNSUPPORTED, "rows %lld bytes apart, more than 2^24", (long long)(stride * size));
   ScanPlan w;
   if (const rsq_status s = plan_scan(p, w)) return s;
   if (w.bytes) {
