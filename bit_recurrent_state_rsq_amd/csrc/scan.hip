@@ -16,12 +16,14 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kL = 64;        // tokens of a chunk
 constexpr int kV = 64;        // state columns of a workgroup
 constexpr int kThreads = 256;
+constexpr int kWide = 1 << 30;   // no power of two
 
 struct ScanArgs {
   SsmArgs s;
@@ -40,6 +42,9 @@ __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x
 __device__ __forceinline__ uint32_t high_pair(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
+
+__device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // An fp32 value as N bf16 pieces. One piece is rounded to nearest-even (2^-9
 // relative). Three pieces hold all 24 bits: each takes the leading 8 of what
@@ -61,7 +66,7 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[N]) {
 
 // A chunk's rows as a buffer: one scalar base, 32-bit offsets, and rows past the
 // sequence's end out of its range, where loads give zeros and stores are dropped.
-// Offsets of lanes without a row or column of their own start at kOutside.
+// A chunk that is asked for has a row (t0 < len). Offsets of lanes without a row or column of their own start at kOutside.
 constexpr uint32_t kOutside = 0x80000000u;
 constexpr int64_t kMaxRowBytes = 1 << 24;   // a chunk then ends below 2^30, and nothing wraps
 struct Rows {
@@ -73,7 +78,7 @@ struct Rows {
     const uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
     const uint32_t high = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
     const uint64_t u = (uint64_t)high << 32 | low;
-    const int rows = min(max(len - t0, 0), kL);
+    const int rows = min(len - t0, kL);   // t0 < len
     rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0,
                                              __builtin_amdgcn_readfirstlane((int)(rows * row_bytes)), 0x00020000);
   }
@@ -111,33 +116,34 @@ struct Vec8 {
     else raw[e >> 2][e & 3] = 0u;
   }
   // an exponent of all ones carries into the sign's place when one is added
-  __device__ __forceinline__ bool any_bad() const {
+  __device__ __forceinline__ uint32_t bad_bits() const {
     uint32_t t = 0;
 #pragma unroll
     for (const auto& r : raw)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         t |= PI == 1 ? (r[i] & 0x7F807F80u) + 0x00800080u : (r[i] & 0x7F800000u) + 0x00800000u;
-    return (t & (PI == 1 ? 0x80008000u : 0x80000000u)) != 0u;
+    return t;
   }
 };
 
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // A tile in LDS: rows of 2^n 16-byte pieces, none padded. Piece p of row r sits
-// at p ^ f(r) of its row, with f such that 16 consecutive rows' pieces p are in
-// 16 different groups of four banks (reads of a fragment's rows), and eight
-// rows' pairs (2 p, 2 p + 1) in eight different pairs of groups (transposed
-// reads). Rows of 128 bytes share the banks with their neighbour, so f then
-// follows from the other bits. f goes by the row modulo 16 only, and pieces are
-// joined by exclusive or: a lane has one address for each kind of access, and
+// at p ^ f(r) of its row, with f such that eight consecutive rows' pairs (2 p,
+// 2 p + 1) are in eight different pairs of groups of four banks (transposed
+// reads), and the lanes that a fragment's 16-byte reads take together (0-3,
+// 12-15, 20-23, 24-27 and the like) are in 16 different groups. Rows of 128
+// bytes share the banks with their neighbour, so f then follows from the other
+// bits. f goes by the row modulo 16 only, and pieces are joined by exclusive or: a lane has one address for each kind of access, and
 // reaches other rows by adding multiples of 16 of them and other pieces by an
 // exclusive or with a constant.
 template <int ROW>   // elements of a row
 struct Tile {
   static constexpr int kBytes = 2 * ROW;
   static __device__ __forceinline__ uint32_t at(int row, int piece) {
-    const int f = ROW >= 128 ? ((row << 1) | ((row >> 3) & 1)) & 15 : ((row & 6) | ((row >> 3) & 1));
+    const int r = row ^ ((row >> 1) & 4);
+    const int f = ROW >= 128 ? ((r << 1) & 14) | ((row >> 3) & 1) : (r & 6) | ((row >> 3) & 1);
     return (uint32_t)(row * kBytes + ((piece ^ f) << 4));
   }
   // a fragment's piece of row lane % 16: pieces 4 i + lane / 16 (exclusive or 64 i)
@@ -192,9 +198,12 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
   __shared__ __attribute__((aligned(16))) uint8_t lds_b[PI * BB];
   __shared__ __attribute__((aligned(16))) uint8_t lds_x[PI * XB];
   __shared__ __attribute__((aligned(16))) uint8_t lds_s[STATES ? 16 : PY * SB];   // S^T: [column][key]
-  // of a chunk's tokens, by the chunk's parity: c_t as a float pair, d_t, and d_t e^{c_L - c_t}
-  __shared__ __attribute__((aligned(16))) float lds_hi[2][kL], lds_lo[2][kL], lds_d[2][kL], lds_w[2][kL];
+  // of a chunk's tokens, by the chunk's parity: d_t e^{c_L - c_t}, and the factors of e^{c_t - c_s}
+  constexpr int LY = STATES ? 4 : kL;
+  __shared__ __attribute__((aligned(16))) float lds_w[2][kL], lds_from[2][LY], lds_to[2][LY];
+  __shared__ __attribute__((aligned(16))) int lds_whole[2][LY];
   __shared__ float lds_decay[2];     // e^{c_L}
+  __shared__ int lds_mid[2];         // the power of two that is shifted, or kWide for none
   __shared__ int lds_first[2][kV];   // first token of a column whose x is not finite
   __shared__ int lds_bad[2];
 
@@ -292,8 +301,8 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
       rc[i].load(rC, at);
     }
   };
-  // a load of fewer than 16 rows (d_k = 256: 8) moves f by the bit of row 8
-  auto flip = [](int rows) { return (uint32_t)((DK >= 128 ? (rows >> 3) & 1 : 0) << 4); };
+  // a load of fewer than 16 rows (d_k = 256: 8) moves f by the bits of row 8
+  auto flip = [](int rows) { return (uint32_t)((rows >> 3) & 1 ? 9 << 4 : 0); };
   uint32_t yoff = (uint32_t)((16 * wave + n16) * yrow + 4 * g * (int)sizeof(T));
   // LDS addresses of this lane
   uint32_t a_bput = TB::at(tid / (DK / 8), tid % (DK / 8)), a_xput = TX::at(tid / (kV / 8), tid % (kV / 8));
@@ -309,7 +318,9 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
       delta = a.s.dt_bias ? dt + a.s.dt_bias[h] : dt;
       if (a.s.softplus) delta = softplus(delta);
     }
+    // a token that decays by 2^-2000 keeps nothing of an fp32 state
     double cum = (double)delta * (double)A2;
+    cum = cum < -2000. ? -2000. : cum > 2000. ? 2000. : cum;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
       const double o = __shfl_up(cum, m, 64);
@@ -317,12 +328,23 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
     }
     const double last = __shfl(cum, 63, 64);
     total += last;
-    const float hi = (float)cum;
-    lds_hi[par][lane] = hi;
-    lds_lo[par][lane] = (float)(cum - (double)hi);
-    lds_d[par][lane] = delta;
     lds_w[par][lane] = __builtin_amdgcn_exp2f((float)(last - cum)) * delta;
     if (lane == 0) lds_decay[par] = __builtin_amdgcn_exp2f((float)last);
+    if constexpr (!STATES) {
+      // c = n + f with n whole: 2^{c_t - c_s} = 2^{f_t} 2^{n_t - n_s} 2^{-f_s}.
+      // Where the n are within kNear of their middle, powers of two shift them
+      // into the factors of t and s; both ways give the same bits.
+      constexpr int kNear = 40;   // the products that the factors scale have 2^87 left
+      const double n = rint(cum);
+      const float f = (float)(cum - n);
+      const int whole = (int)n, mid = (int)rint(0.5 * last);
+      const bool narrow = __builtin_amdgcn_ballot_w64(!(fabs(cum - 0.5 * last) < kNear)) == 0;
+      const int shift = narrow ? mid - whole : 0;
+      lds_from[par][lane] = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(-f) * delta, shift);
+      lds_to[par][lane] = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), -shift);
+      lds_whole[par][lane] = whole;
+      if (lane == 0) lds_mid[par] = narrow ? mid : kWide;
+    }
   };
   const T* dtp = reinterpret_cast<const T*>(a.s.dt) + begin * a.s.dt_stride + h;
   auto load_dt = [&](int t0) { return t0 + lane < len ? to_f32(dtp[(int64_t)(t0 + lane) * a.s.dt_stride]) : 0.f; };
@@ -352,22 +374,33 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
     }
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-      // A product with x_s takes every s of a chunk, weights of later tokens
-      // being zero: an infinity or a NaN there would reach earlier tokens. It
-      // is taken out, and its column is NaN from its token on.
-      if (rx[i].any_bad()) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (rx[i].bad(e)) {
-            rx[i].clear(e);
-            atomicMin(&lds_first[par][xv8 + e], tid / (kV / 8) + i * RX);
-          }
-        lds_bad[par] = 1;
-      }
       u32x4 p[PI];
       rx[i].pieces(p);
 #pragma unroll
       for (int q = 0; q < PI; ++q) *reinterpret_cast<u32x4*>(lds_x + q * XB + i * RX * TX::kBytes + a_xput) = p[q];
+    }
+    // A product with x_s takes every s of a chunk, weights of later tokens
+    // being zero: an infinity or a NaN there would reach earlier tokens. It is
+    // taken out, and its column is NaN from its token on.
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < NX; ++i) odd |= rx[i].bad_bits();
+    if (odd & (PI == 1 ? 0x80008000u : 0x80000000u)) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        Vec8<T, PI> v = rx[i];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (v.bad(e)) {
+            v.clear(e);
+            atomicMin(&lds_first[par][xv8 + e], tid / (kV / 8) + i * RX);
+          }
+        u32x4 p[PI];
+        v.pieces(p);
+#pragma unroll
+        for (int q = 0; q < PI; ++q) *reinterpret_cast<u32x4*>(lds_x + q * XB + i * RX * TX::kBytes + a_xput) = p[q];
+      }
+      lds_bad[par] = 1;
     }
     if constexpr (!STATES) {
 #pragma unroll
@@ -396,7 +429,10 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
 #pragma unroll
       for (int i = 0; i < KS; ++i) rc[i].pieces(cf[i]);
       const int tt = 16 * wave + n16;   // this lane's token
-      const float chi = lds_hi[par][tt], clo = lds_lo[par][tt];
+      const int mid = __builtin_amdgcn_readfirstlane(lds_mid[par]);
+      // y = to_t (2^{n} S^T C + P X), n the middle's power or this token's own
+      const float to = lds_to[par][tt];
+      const int power = mid == kWide ? lds_whole[par][tt] : mid;
       // ---- P^T (rows s, columns t), tile by tile up to the diagonal
       u32x4 pf[kL / 32][PY];
 #pragma unroll
@@ -415,12 +451,14 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
               for (int q = 0; q < PI; ++q)
                 if (p + q < 3) acc = mfma(bf, cf[i][q], acc);
             }
-          const f32x4 shi = *reinterpret_cast<const f32x4*>(&lds_hi[par][16 * j + 4 * g]);
-          const f32x4 slo = *reinterpret_cast<const f32x4*>(&lds_lo[par][16 * j + 4 * g]);
-          const f32x4 sd = *reinterpret_cast<const f32x4*>(&lds_d[par][16 * j + 4 * g]);
+          const f32x4 from = *reinterpret_cast<const f32x4*>(&lds_from[par][16 * j + 4 * g]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[r] *= __builtin_amdgcn_exp2f((chi - shi[r]) + (clo - slo[r])) * sd[r];
+          for (int r = 0; r < 4; ++r) acc[r] *= from[r];
+          if (mid == kWide) {
+            const i32x4 n = *reinterpret_cast<const i32x4*>(&lds_whole[par][16 * j + 4 * g]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = __builtin_amdgcn_ldexpf(acc[r], power - n[r]);
+          }
           if (j == wave) {   // later tokens: out, whatever their weight
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[r] = 4 * g + r <= n16 ? acc[r] : 0.f;
@@ -433,8 +471,8 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
         __builtin_amdgcn_sched_barrier(0);
       }
       // ---- y^T (rows v, columns t)
-      const float et = __builtin_amdgcn_exp2f(chi + clo);
       const Rows rY(y, yrow, t0, len);
+      const float before = __builtin_amdgcn_ldexpf(1.f, power);
 #pragma unroll
       for (int vt = 0; vt < kV / 16; ++vt) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -448,7 +486,7 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
               if (p + q < 3) acc = mfma(sf, cf[i][q], acc);
           }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] *= et;
+        for (int r = 0; r < 4; ++r) acc[r] *= before;
 #pragma unroll
         for (int j2 = 0; j2 < kL / 32; ++j2) {
           if (2 * j2 <= wave) {
@@ -462,16 +500,17 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
           }
         }
         // D x, from the pieces of x (their sum is exact)
-        float xv[4] = {0.f, 0.f, 0.f, 0.f};
+        float xv[4];
 #pragma unroll
         for (int p = PI - 1; p >= 0; --p) {
           const u32x2 w = *reinterpret_cast<const u32x2*>(lds_x + p * XB + (a_xown ^ (vt << 5)));
-          xv[0] += __uint_as_float(w[0] << 16), xv[1] += __uint_as_float(w[0] & 0xFFFF0000u);
-          xv[2] += __uint_as_float(w[1] << 16), xv[3] += __uint_as_float(w[1] & 0xFFFF0000u);
+          const float part[4] = {low_half(w[0]), high_half(w[0]), low_half(w[1]), high_half(w[1])};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) xv[r] = p == PI - 1 ? part[r] : xv[r] + part[r];
         }
         float out[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], acc[r]);
+        for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], acc[r] * to);
         if (bad) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -504,12 +543,9 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
       u32x4 xw[PW];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float lo = 0.f, hi = 0.f;
+        float lo = low_half(xr[PI - 1][i]), hi = high_half(xr[PI - 1][i]);
 #pragma unroll
-        for (int p = PI - 1; p >= 0; --p) {
-          lo += __uint_as_float(xr[p][i] << 16);
-          hi += __uint_as_float(xr[p][i] & 0xFFFF0000u);
-        }
+        for (int p = PI - 2; p >= 0; --p) lo += low_half(xr[p][i]), hi += high_half(xr[p][i]);
         lo *= i < 2 ? w0[2 * i] : w1[2 * i - 4];
         hi *= i < 2 ? w0[2 * i + 1] : w1[2 * i - 3];
         uint32_t p3[PW];
