@@ -35,6 +35,12 @@ FLAGS = [
     "-Wno-unused-result",
 ]
 
+# Matrix products keep their results in vector registers here. With results in
+# accumulation registers (which the compiler picks for kernels of low occupancy)
+# it was seen to read them too early behind a branch.
+VGPR_RESULTS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+SOURCE_FLAGS = {"scan.hip": VGPR_RESULTS, "w4.hip": VGPR_RESULTS}
+
 
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
@@ -42,7 +48,7 @@ def sources():
 
 def _compile(src):
     obj = os.path.join(OBJ, os.path.basename(src) + ".o")
-    cmd = [HIPCC] + FLAGS + ["-c", src, "-o", obj]
+    cmd = [HIPCC] + FLAGS + SOURCE_FLAGS.get(os.path.basename(src), []) + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     errs = "\n".join(l for l in (r.stdout + r.stderr).splitlines()
                      if "packed-fp32-ops" not in l)

@@ -6,9 +6,9 @@
 //
 // A read and a write of every element against 2 W operations: bound by memory.
 // A lane owns 16 bytes of consecutive channels, so that a wavefront reads 1 KB
-// runs, and walks kTile tokens with the last W - 1 inputs in registers; a tile
-// reads W - 1 rows again (from L2). The rows of a tile are loaded kAhead at a
-// time before the first is used.
+// runs, and walks a tile of tokens with the last W - 1 inputs in registers; a tile
+// reads W - 1 rows again (from L2). The next kAhead rows are loaded while the
+// last ones are worked on, and kept as they come (bf16 pairs) until then.
 #include <type_traits>
 
 #include "host_util.hpp"
@@ -17,8 +17,7 @@
 namespace rsq {
 namespace {
 
-constexpr int kTile = 32;   // tokens of a wavefront
-constexpr int kAhead = 8;   // rows in flight
+constexpr int kAhead = 4;   // rows loaded ahead
 constexpr int kWaves = 4;   // wavefronts of a block, each with a tile of its own
 
 struct ConvArgs {
@@ -31,6 +30,7 @@ struct ConvArgs {
   Sequences q;
   int32_t C;
   int32_t cblocks, tiles;   // blocks along the channels; blocks along a sequence
+  int32_t tile;             // tokens of a wavefront
 };
 
 // exp(-v) saturates to infinity for v below about -88, where silu(v) rounds to
@@ -59,6 +59,29 @@ __device__ __forceinline__ void load_row(const T* p, float (&v)[VEC]) {
   if constexpr (VEC == 1) v[0] = to_f32(p[0]);
   else load_vec<VEC>(p, v);
 }
+
+// a row's VEC elements as loaded
+template <typename T, int VEC>
+struct RawRow {
+  uint32_t w[VEC == 1 ? 1 : 4];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == 1) {
+      w[0] = sizeof(T) == 2 ? *reinterpret_cast<const uint16_t*>(p) : *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      const uint4 t = *reinterpret_cast<const uint4*>(p);
+      w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[VEC]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = __uint_as_float(w[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = __uint_as_float((e & 1) ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+    }
+  }
+};
 
 template <typename T, int VEC>
 __device__ __forceinline__ void store_row(T* p, const float (&v)[VEC]) {
@@ -129,7 +152,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompt_kernel(ConvArgs a) {
   const int s = (int)(id / a.tiles);
   int64_t len;
   const int64_t begin = seq_range(a.q, s, len);
-  const int64_t t0 = (tile * kWaves + wave) * kTile;
+  const int64_t t0 = (tile * kWaves + wave) * a.tile;
   const int c = (cb * 64 + lane) * VEC;
   if (c >= a.C || t0 >= len) return;   // (an empty sequence keeps its state)
   const T* x = reinterpret_cast<const T*>(a.x) + begin * a.x_stride + c;
@@ -138,14 +161,17 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompt_kernel(ConvArgs a) {
   float w[VEC][W], b[VEC];
   load_params<W, VEC>(a, c, w, b);
   float win[W][VEC];   // win[W - 1] is the current input
-  float old[W - 1][VEC];
-  if (t0 == 0) {
-    if (st) load_state<T, W, VEC>(st, old);
+  auto before = [&](float (&h)[W - 1][VEC]) {
+    if (st) load_state<T, W, VEC>(st, h);
     else
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) old[j][e] = 0.f;
+        for (int e = 0; e < VEC; ++e) h[j][e] = 0.f;
+  };
+  if (t0 == 0) {
+    float old[W - 1][VEC];
+    before(old);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -154,20 +180,27 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompt_kernel(ConvArgs a) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_row<T, VEC>(x + (t0 - (W - 1) + j) * a.x_stride, win[j]);
   }
-  const int n = (int)(len - t0 < kTile ? len - t0 : kTile);
-  for (int i0 = 0; i0 < n; i0 += kAhead) {
-    float rows[kAhead][VEC];
+  const int n = (int)(len - t0 < a.tile ? len - t0 : a.tile);
+  x += t0 * a.x_stride;
+  y += t0 * a.y_stride;
+  RawRow<T, VEC> rows[kAhead], next[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (i0 + i < n) load_row<T, VEC>(x + (t0 + i0 + i) * a.x_stride, rows[i]);
+  for (int i = 0; i < kAhead; ++i) next[i].load(x + (int64_t)(i < n ? i : n - 1) * a.x_stride);
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) rows[i] = next[i];
+    if (i0 + kAhead < n) {
+      // (past the last row, that row again)
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) next[i].load(x + (int64_t)(i0 + kAhead + i < n ? i0 + kAhead + i : n - 1) * a.x_stride);
+    }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i < n) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) win[W - 1][e] = rows[i][e];
+        rows[i].get(win[W - 1]);
         float out[VEC];
         conv_out<T, W, VEC, SILU>(win, w, b, out);
-        store_row<T, VEC>(y + (t0 + i0 + i) * a.y_stride, out);
+        store_row<T, VEC>(y + (int64_t)(i0 + i) * a.y_stride, out);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -175,25 +208,27 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompt_kernel(ConvArgs a) {
       }
     }
   }
-  // The lane of the first tile is the only reader of this state, and it has
-  // read it: it writes the new one too. Inputs t < 0 are the old state's.
+  // The lane of the first tile is the only reader of this state, and it writes
+  // the new one. Inputs t < 0 are the old state's.
   if (t0 == 0 && st) {
-    float next[W - 1][VEC];
+    float old[W - 1][VEC];
+    if (len < W - 1) before(old);
+    float last[W - 1][VEC];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       const int64_t t = len - (W - 1) + j;
       if (t >= 0) {
-        load_row<T, VEC>(x + t * a.x_stride, next[j]);
+        load_row<T, VEC>(x + t * a.x_stride, last[j]);   // (x is the sequence's first row: t0 = 0)
       } else {
         // t + W - 1 = len + j with 0 < len < W - 1
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
           if (k == (int)(len + j))
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) next[j][e] = old[k][e];
+            for (int e = 0; e < VEC; ++e) last[j][e] = old[k][e];
       }
     }
-    store_state<T, W, VEC>(st, next);
+    store_state<T, W, VEC>(st, last);
   }
 }
 
@@ -297,7 +332,12 @@ extern "C" rsq_status rsq_causal_conv(const rsq_conv* p, void* stream) {
   a.q = Sequences{p->offsets, p->tokens, p->max_len, p->seqs};
   a.C = p->channels;
   a.cblocks = (int32_t)ceil_div(C, 64 * v);
-  a.tiles = (int32_t)ceil_div(p->max_len, kTile * kWaves);
+  // Tiles of 32 tokens re-read 3 rows of 35; where they leave the chip short of
+  // wavefronts (16 for each of 256 compute units), shorter ones wait less: 1531 x
+  // 1031 fp32 one element a lane 9.6 us with 32, 6.9 with 8.
+  a.tile = 32;
+  while (a.tile > 8 && a.cblocks * ceil_div(p->tokens, a.tile) < 4096) a.tile /= 2;
+  a.tiles = (int32_t)ceil_div(p->max_len, (int64_t)a.tile * kWaves);
   const int64_t blocks = token ? ceil_div(p->seqs * ceil_div(C, v), 256) : (int64_t)a.cblocks * a.tiles * p->seqs;
   if (blocks > kMaxGrid) return fail(RSQ_E_UNSUPPORTED, "%lld workgroups", (long long)blocks);
   ConvFn fn;

@@ -178,6 +178,41 @@ __device__ __forceinline__ u32x4 read_tr8(const uint8_t* p) {
 // each for dozens of addresses costs more than the operation that makes them.
 __device__ __forceinline__ void local(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
+// One step of a running sum over lanes: the lane that CTRL names, in the rows of
+// 16 lanes that ROWS has, zero elsewhere.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double scan_step(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// sum over the lanes up to this one
+__device__ __forceinline__ double wave_scan(double v) {
+  v = scan_step<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
+  v = scan_step<0x112, 0xF>(v);
+  v = scan_step<0x114, 0xF>(v);
+  v = scan_step<0x118, 0xF>(v);
+  v = scan_step<0x142, 0xA>(v);   // lane 15 of a row to the next row (rows 1 and 3)
+  return scan_step<0x143, 0xC>(v);   // lane 31 to rows 2 and 3
+}
+__device__ __forceinline__ double lane63(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// A matrix product's result may be read by other instructions only some cycles
+// after its issue. The compiler counts them out, but was seen not to across a
+// branch, with the result in accumulation registers: the build keeps results out
+// of those, and the places where a branch follows wait here besides.
+__device__ __forceinline__ void settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // PI pieces of the inputs, PY of the computed factors of y (P and S), 3 of the
 // weighted x that enters the state (a state stays exact to fp32). Products of
 // pieces below 2^-24 are left out.
@@ -189,7 +224,7 @@ __device__ __forceinline__ void local(uint32_t& v) { asm volatile("" : "+v"(v));
 // segment before the last, scanned first so that the segments can run side by
 // side).
 template <typename T, int DK, int PI, int PY, bool STATES>
-__global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2 : 3) void scan_kernel(ScanArgs a) {
   constexpr int PW = 3;
   constexpr int KT = DK / 16, KS = DK / 32;
   typedef Tile<DK> TB;
@@ -321,12 +356,8 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
     // a token that decays by 2^-2000 keeps nothing of an fp32 state
     double cum = (double)delta * (double)A2;
     cum = cum < -2000. ? -2000. : cum > 2000. ? 2000. : cum;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const double o = __shfl_up(cum, m, 64);
-      if (lane >= m) cum += o;
-    }
-    const double last = __shfl(cum, 63, 64);
+    cum = wave_scan(cum);
+    const double last = lane63(cum);
     total += last;
     lds_w[par][lane] = __builtin_amdgcn_exp2f((float)(last - cum)) * delta;
     if (lane == 0) lds_decay[par] = __builtin_amdgcn_exp2f((float)last);
@@ -351,10 +382,14 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
 
   const int c_end = min(chunks, (seg + 1) * a.seg_chunks);
   int c = seg * a.seg_chunks;
+  float dt_next = 0.f;   // of wavefront 0: dt of the chunk after this one
   if (c < c_end) {
     load_bx(c * kL);
     load_c(c * kL);
-    if (wave == 0) decays(load_dt(c * kL), c * kL, c & 1);
+    if (wave == 0) {
+      dt_next = load_dt((c + 1) * kL);
+      decays(load_dt(c * kL), c * kL, c & 1);
+    }
   }
   if (tid < 2 * kV) lds_first[tid / kV][tid % kV] = kL;
   if (tid < 2) lds_bad[tid] = 0;
@@ -416,10 +451,15 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
     __syncthreads();
     const bool bad = __builtin_amdgcn_readfirstlane(lds_bad[par]) != 0;
     const bool more = c + 1 < c_end;
-    float dt_next = 0.f;
     if (more) {
-      load_bx(t0 + kL);
-      if (wave == 0) dt_next = load_dt(t0 + kL);
+      if (wave == 0) {
+        const float dt = dt_next;
+        dt_next = load_dt(t0 + 2 * kL);
+        load_bx(t0 + kL);
+        decays(dt, t0 + kL, par ^ 1);
+      } else {
+        load_bx(t0 + kL);
+      }
     }
     if (tid < kV) lds_first[par ^ 1][tid] = kL;
     if (tid == kV) lds_bad[par ^ 1] = 0;
@@ -433,95 +473,115 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
       // y = to_t (2^{n} S^T C + P X), n the middle's power or this token's own
       const float to = lds_to[par][tt];
       const int power = mid == kWide ? lds_whole[par][tt] : mid;
-      // ---- P^T (rows s, columns t), tile by tile up to the diagonal
+      // ---- P^T (rows s, columns t), two tiles (a k-step of y) at a time, up to
+      // the diagonal's; two chains of dependent products run side by side
       u32x4 pf[kL / 32][PY];
 #pragma unroll
-      for (int j = 0; j < kL / 16; ++j) {
-        uint32_t lo[PY], hi[PY];
-#pragma unroll
-        for (int q = 0; q < PY; ++q) lo[q] = hi[q] = 0u;
-        if (j <= wave) {
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int j2 = 0; j2 < kL / 32; ++j2) {
+        if (2 * j2 <= wave) {
+          f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
           for (int i = 0; i < KS; ++i)
 #pragma unroll
-            for (int p = 0; p < PI; ++p) {
-              const u32x4 bf = *reinterpret_cast<const u32x4*>(lds_b + p * BB + 16 * j * TB::kBytes + (a_frag ^ (i << 6)));
+            for (int p = 0; p < PI; ++p)
 #pragma unroll
-              for (int q = 0; q < PI; ++q)
-                if (p + q < 3) acc = mfma(bf, cf[i][q], acc);
+              for (int e = 0; e < 2; ++e) {
+                const u32x4 bf = *reinterpret_cast<const u32x4*>(lds_b + p * BB + (32 * j2 + 16 * e) * TB::kBytes +
+                                                                 (a_frag ^ (i << 6)));
+#pragma unroll
+                for (int q = 0; q < PI; ++q)
+                  if (p + q < 3) acc[e] = mfma(bf, cf[i][q], acc[e]);
+              }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int s0 = 32 * j2 + 16 * e;
+            const f32x4 from = *reinterpret_cast<const f32x4*>(&lds_from[par][s0 + 4 * g]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[e][r] *= from[r];
+            if (mid == kWide) {
+              const i32x4 n = *reinterpret_cast<const i32x4*>(&lds_whole[par][s0 + 4 * g]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[e][r] = __builtin_amdgcn_ldexpf(acc[e][r], power - n[r]);
             }
-          const f32x4 from = *reinterpret_cast<const f32x4*>(&lds_from[par][16 * j + 4 * g]);
+            if (2 * j2 + 1 >= wave) {   // later tokens: out, whatever their weight
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] *= from[r];
-          if (mid == kWide) {
-            const i32x4 n = *reinterpret_cast<const i32x4*>(&lds_whole[par][16 * j + 4 * g]);
+              for (int r = 0; r < 4; ++r) acc[e][r] = s0 + 4 * g + r <= tt ? acc[e][r] : 0.f;
+            }
+            uint32_t lo[PY], hi[PY];
+            split_pair<PY>(acc[e][0], acc[e][1], lo);
+            split_pair<PY>(acc[e][2], acc[e][3], hi);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] = __builtin_amdgcn_ldexpf(acc[r], power - n[r]);
+            for (int q = 0; q < PY; ++q) pf[j2][q][2 * e] = lo[q], pf[j2][q][2 * e + 1] = hi[q];
           }
-          if (j == wave) {   // later tokens: out, whatever their weight
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] = 4 * g + r <= n16 ? acc[r] : 0.f;
-          }
-          split_pair<PY>(acc[0], acc[1], lo);
-          split_pair<PY>(acc[2], acc[3], hi);
         }
-#pragma unroll
-        for (int q = 0; q < PY; ++q) pf[j / 2][q][2 * (j & 1)] = lo[q], pf[j / 2][q][2 * (j & 1) + 1] = hi[q];
         __builtin_amdgcn_sched_barrier(0);
       }
-      // ---- y^T (rows v, columns t)
+      // ---- y^T (rows v, columns t), VN tiles of v at a time
+      constexpr int VN = PI == 1 && DK <= 128 ? 2 : 1;
       const Rows rY(y, yrow, t0, len);
       const float before = __builtin_amdgcn_ldexpf(1.f, power);
 #pragma unroll
-      for (int vt = 0; vt < kV / 16; ++vt) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int vp = 0; vp < kV / 16; vp += VN) {
+        f32x4 acc[VN];
+#pragma unroll
+        for (int e = 0; e < VN; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
-          for (int p = 0; p < PY; ++p) {
-            const u32x4 sf = *reinterpret_cast<const u32x4*>(lds_s + p * SB + 16 * vt * TB::kBytes + (a_frag ^ (i << 6)));
+          for (int p = 0; p < PY; ++p)
 #pragma unroll
-            for (int q = 0; q < PI; ++q)
-              if (p + q < 3) acc = mfma(sf, cf[i][q], acc);
-          }
+            for (int e = 0; e < VN; ++e) {
+              const u32x4 sf = *reinterpret_cast<const u32x4*>(lds_s + p * SB + 16 * (vp + e) * TB::kBytes + (a_frag ^ (i << 6)));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] *= before;
+              for (int q = 0; q < PI; ++q)
+                if (p + q < 3) acc[e] = mfma(sf, cf[i][q], acc[e]);
+            }
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[e][r] *= before;
 #pragma unroll
         for (int j2 = 0; j2 < kL / 32; ++j2) {
           if (2 * j2 <= wave) {
 #pragma unroll
-            for (int p = 0; p < PI; ++p) {
-              const u32x4 xf = read_tr8<kV>(lds_x + p * XB + 32 * j2 * TX::kBytes + (a_xtr ^ (vt << 5)));
+            for (int p = 0; p < PI; ++p)
 #pragma unroll
-              for (int q = 0; q < PY; ++q)
-                if (p + q < 3) acc = mfma(xf, pf[j2][q], acc);
-            }
+              for (int e = 0; e < VN; ++e) {
+                const u32x4 xf = read_tr8<kV>(lds_x + p * XB + 32 * j2 * TX::kBytes + (a_xtr ^ ((vp + e) << 5)));
+#pragma unroll
+                for (int q = 0; q < PY; ++q)
+                  if (p + q < 3) acc[e] = mfma(xf, pf[j2][q], acc[e]);
+              }
           }
         }
-        // D x, from the pieces of x (their sum is exact)
-        float xv[4];
+        settle();
 #pragma unroll
-        for (int p = PI - 1; p >= 0; --p) {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(lds_x + p * XB + (a_xown ^ (vt << 5)));
-          const float part[4] = {low_half(w[0]), high_half(w[0]), low_half(w[1]), high_half(w[1])};
+        for (int e = 0; e < VN; ++e) {
+          const int vt = vp + e;
+          // D x, from the pieces of x (their sum is exact)
+          float xv[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) xv[r] = p == PI - 1 ? part[r] : xv[r] + part[r];
+          for (int p = PI - 1; p >= 0; --p) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(lds_x + p * XB + (a_xown ^ (vt << 5)));
+            const float part[4] = {low_half(w[0]), high_half(w[0]), low_half(w[1]), high_half(w[1])};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) xv[r] = p == PI - 1 ? part[r] : xv[r] + part[r];
+          }
+          float out[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], acc[e][r] * to);
+          if (bad) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (tt >= lds_first[par][16 * vt + 4 * g + r]) out[r] = __builtin_nanf("");
+          }
+          uint32_t at = yoff + (uint32_t)(16 * vt * sizeof(T));
+          if (v0 + kV > dv) at = v0 + 16 * vt + 4 * g < dv ? at : kOutside;
+          if constexpr (PI == 1)
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(out[0], out[1]), bf16_pair(out[2], out[3])}, rY.rsrc, (int)at, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{out[0], out[1], out[2], out[3]}), rY.rsrc, (int)at, 0, 0);
         }
-        float out[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], acc[r] * to);
-        if (bad) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (tt >= lds_first[par][16 * vt + 4 * g + r]) out[r] = __builtin_nanf("");
-        }
-        uint32_t at = yoff + (uint32_t)(16 * vt * sizeof(T));
-        if (v0 + kV > dv) at = v0 + 16 * vt + 4 * g < dv ? at : kOutside;
-        if constexpr (PI == 1)
-          __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(out[0], out[1]), bf16_pair(out[2], out[3])}, rY.rsrc, (int)at, 0, 0);
-        else
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{out[0], out[1], out[2], out[3]}), rY.rsrc, (int)at, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (more) load_c(t0 + kL);
@@ -553,23 +613,24 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
 #pragma unroll
         for (int q = 0; q < PW; ++q) xw[q][i] = p3[q];
       }
+      // four tiles of keys side by side
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
+      for (int k4 = 0; k4 < KT; k4 += 4) {
 #pragma unroll
         for (int p = 0; p < PI; ++p) {
-          const u32x4 bf = read_tr8<DK>(lds_b + p * BB + 32 * ts * TB::kBytes + (a_btr ^ (kt << 5)));
+          u32x4 bf[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bf[e] = read_tr8<DK>(lds_b + p * BB + 32 * ts * TB::kBytes + (a_btr ^ ((k4 + e) << 5)));
 #pragma unroll
           for (int q = 0; q < PW; ++q)
-            if (p + q < 3) S[kt] = mfma(bf, xw[q], S[kt]);
-          if (kt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (p + q < 3) S[k4 + e] = mfma(bf[e], xw[q], S[k4 + e]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    // A matrix product's result may be read by other instructions only some
-    // cycles after its issue. The compiler counts them out, but was seen not to
-    // across the branch below (with S in accumulation registers).
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_nop 15");
-    __builtin_amdgcn_sched_barrier(0);
+    settle();
     if (bad) {
       if (lds_first[par][16 * wave + n16] < kL) {
 #pragma unroll
@@ -578,7 +639,6 @@ __global__ __launch_bounds__(kThreads, DK > 128 || PI > 1 ? 1 : 3) void scan_ker
           for (int r = 0; r < 4; ++r) S[kt][r] = __builtin_nanf("");
       }
     }
-    if (wave == 0 && more) decays(dt_next, t0 + kL, par ^ 1);
     __syncthreads();   // the chunk's LDS has been read
   }
 

@@ -83,7 +83,46 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(PackArgs a) {
     reinterpret_cast<float*>(a.out_scales)[s] = in ? reinterpret_cast<const float*>(a.scales)[n * (a.K / a.group) + gr] : 0.f;
 }
 
-// Eight consecutive columns of a row of x for one product of 32 columns.
+constexpr int x_size(int xt) { return xt == kXF32 ? 4 : xt == kXBf16 ? 2 : 1; }
+
+// Eight consecutive columns of a row of x for one product of 32 columns, as loaded.
+template <int XT>
+struct XRaw {
+  static constexpr int kSize = x_size(XT), kWords = 2 * kSize;
+  uint32_t w[kWords];
+  // zeros past the last row and column (K is a multiple of 32: a run of eight
+  // columns is inside or outside)
+  __device__ __forceinline__ void load(const W4Args& a, int64_t row, int64_t k, bool wide) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x) + (row * a.x_stride + k) * kSize;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    if (row < a.M && k < a.K) {
+      if (wide) {
+        if constexpr (kSize == 1) {
+          const uint2 t = *reinterpret_cast<const uint2*>(p);
+          w[0] = t.x, w[1] = t.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kSize / 2; ++i) {
+            const uint4 t = reinterpret_cast<const uint4*>(p)[i];
+            w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
+          }
+        }
+      } else if constexpr (kSize == 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
+      } else if constexpr (kSize == 2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+      }
+    }
+  }
+};
+
+// ... and as the product takes them
 template <int XT>
 struct XFrag {
   static constexpr int kPieces = XT == kXF32 ? 3 : 1;
@@ -91,36 +130,8 @@ struct XFrag {
 };
 
 template <int XT>
-__device__ __forceinline__ void load_x(const W4Args& a, int64_t row, int64_t k, bool wide, XFrag<XT>& f) {
-  constexpr int size = XT == kXF32 ? 4 : XT == kXBf16 ? 2 : 1;
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x) + (row * a.x_stride + k) * size;
-  uint32_t w[2 * size];
-#pragma unroll
-  for (int i = 0; i < 2 * size; ++i) w[i] = 0u;
-  if (row < a.M && k < a.K) {
-    // K is a multiple of 32: a run of eight columns is inside or outside
-    if (wide) {
-      if constexpr (size == 1) {
-        const uint2 t = *reinterpret_cast<const uint2*>(p);
-        w[0] = t.x, w[1] = t.y;
-      } else {
-#pragma unroll
-        for (int i = 0; i < size / 2; ++i) {
-          const uint4 t = reinterpret_cast<const uint4*>(p)[i];
-          w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
-        }
-      }
-    } else if constexpr (size == 1) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
-    } else if constexpr (size == 2) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = reinterpret_cast<const uint32_t*>(p)[e];
-    }
-  }
+__device__ __forceinline__ void convert_x(const XRaw<XT>& r, XFrag<XT>& f) {
+  const auto& w = r.w;
   if constexpr (XT == kXBf16) {
     f.p[0] = u32x4{w[0], w[1], w[2], w[3]};
   } else if constexpr (XT == kXF32) {
@@ -148,6 +159,35 @@ __device__ __forceinline__ void load_x(const W4Args& a, int64_t row, int64_t k, 
   }
 }
 
+// What a wavefront loads for a block of 128 columns: the codes and scales of NT
+// tiles and, when AHEAD, the first 16 rows of x.
+template <int XT, int GPB, int NT, bool AHEAD>
+struct Block {
+  u32x4 w[NT];
+  uint32_t s[NT][GPB];   // scales as stored
+  XRaw<XT> x[AHEAD ? 4 : 1];
+  __device__ __forceinline__ void load(const W4Args& a, int tile0, int kb, int64_t m0, int lane, bool wide) {
+    const int n16 = lane & 15, g = lane >> 4, tiles = a.npad >> 4;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = tile0 + i < tiles ? tile0 + i : tiles - 1;   // a tile past the last is not stored
+      w[i] = *reinterpret_cast<const u32x4*>(a.codes + ((size_t)t * a.kblocks + kb) * 1024 + lane * 16);
+#pragma unroll
+      for (int q = 0; q < GPB; ++q) {
+        const size_t at = (size_t)(kb * GPB + q) * a.npad + 16 * t + n16;
+        s[i][q] = a.scale_f16 ? reinterpret_cast<const uint16_t*>(a.scales)[at] : reinterpret_cast<const uint32_t*>(a.scales)[at];
+      }
+    }
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j].load(a, m0 + n16, (int64_t)kb * 128 + 32 * j + 8 * g, wide);
+    }
+  }
+  __device__ __forceinline__ float scale(const W4Args& a, int i, int q) const {
+    return a.scale_f16 ? __half2float(__ushort_as_half((uint16_t)s[i][q])) : __uint_as_float(s[i][q]);
+  }
+};
+
 // the eight codes of a word as bf16 numbers 24 + c, in column order
 __device__ __forceinline__ u32x4 codes_bf16(uint32_t w) {
   constexpr uint32_t m = 0x00780078u, b = 0x41C041C0u;   // 16 + 8 (sign bit flipped)
@@ -167,9 +207,8 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
   const int n16 = lane & 15, g = lane >> 4;
   const int tile0 = blockIdx.x * NT;
   const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int tiles = a.npad >> 4;
-  constexpr int size = XT == kXF32 ? 4 : XT == kXBf16 ? 2 : 1;
-  const bool wide = a.x_stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+  constexpr bool AHEAD = MT == 1;
+  const bool wide = a.x_stride * x_size(XT) % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
 
   f32x4 y[NT][MT];
 #pragma unroll
@@ -177,25 +216,30 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) y[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  Block<XT, GPB, NT, AHEAD> next;
+  if (wave < a.kblocks) next.load(a, tile0, wave, m0, lane, wide);
   for (int kb = wave; kb < a.kblocks; kb += WAVES) {
-    u32x4 w[NT];
+    const Block<XT, GPB, NT, AHEAD> b = next;
+    if (kb + WAVES < a.kblocks) next.load(a, tile0, kb + WAVES, m0, lane, wide);
+    const auto& w = b.w;
     float s[NT][GPB];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int t = tile0 + i < tiles ? tile0 + i : tiles - 1;   // a tile past the last is not stored
-      w[i] = *reinterpret_cast<const u32x4*>(a.codes + ((size_t)t * a.kblocks + kb) * 1024 + lane * 16);
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int q = 0; q < GPB; ++q) {
-        const size_t at = (size_t)(kb * GPB + q) * a.npad + 16 * t + n16;
-        s[i][q] = a.scale_f16 ? __half2float(reinterpret_cast<const __half*>(a.scales)[at])
-                              : reinterpret_cast<const float*>(a.scales)[at];
-      }
-    }
+      for (int q = 0; q < GPB; ++q) s[i][q] = b.scale(a, i, q);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       XFrag<XT> x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load_x<XT>(a, m0 + 16 * m + n16, (int64_t)kb * 128 + 32 * j + 8 * g, wide, x[j]);
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (AHEAD) {
+          convert_x(b.x[j], x[j]);
+        } else {
+          XRaw<XT> r;
+          r.load(a, m0 + 16 * m + n16, (int64_t)kb * 128 + 32 * j + 8 * g, wide);
+          convert_x(r, x[j]);
+        }
+      }
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
         // scales of this lane's four rows of x in this group
@@ -289,7 +333,7 @@ template <int XT, int GROUP>
 W4Pick pick_shape(int M, int tiles) {
   // few weight rows: more wavefronts share a tile's columns
   if (M <= 16) {
-    if (tiles >= 1024) return {w4_kernel<XT, GROUP, 2, 1, 4>, 2, 1, 4};
+    if (tiles >= 1024) return {w4_kernel<XT, GROUP, 4, 1, 8>, 4, 1, 8};
     if (tiles >= 384) return {w4_kernel<XT, GROUP, 1, 1, 8>, 1, 1, 8};
     return {w4_kernel<XT, GROUP, 1, 1, 16>, 1, 1, 16};
   }
