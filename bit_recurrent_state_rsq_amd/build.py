@@ -1,4 +1,5 @@
-"""Build librsq.so (the HIP kernels and the C ABI of include/rsq.h) for gfx950.
+"""Build librsq.so (the HIP kernels and the C ABI of include/rsq.h) for gfx950,
+and _binding.so (host code: torch tensors as arguments of the layer operators).
 
 Run as `python bit_recurrent_state_rsq_amd/build.py` (a plain script: it does
 not import the package, which would load the library it is about to rebuild).
@@ -57,11 +58,37 @@ def _compile(src):
     return obj
 
 
+def _binding():
+    """_binding.so: a Python extension against torch's C++ headers, without device code."""
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    out = os.path.join(PKG, "_binding.so")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % _torch_abi(),
+           "-I" + os.path.join(ROOT, "include"), "-I" + os.path.join(torch, "include"),
+           "-I" + os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", out + ".tmp",
+           "-L" + os.path.join(torch, "lib"), "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("binding.cpp failed:\n" + r.stdout + r.stderr)
+    os.replace(out + ".tmp", out)
+
+
+def _torch_abi():
+    """Which std::string the installed torch was built with."""
+    import torch
+    return int(torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
 def build(verbose=True):
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_binding)
         objs = list(ex.map(_compile, srcs))
+        binding.result()
     tmp = OUT + ".tmp"
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -334,7 +334,7 @@ W4Pick pick_shape(int M, int tiles) {
   // few weight rows: more wavefronts share a tile's columns
   if (M <= 16) {
     if (tiles >= 1024) return {w4_kernel<XT, GROUP, 4, 1, 8>, 4, 1, 8};
-    if (tiles >= 384) return {w4_kernel<XT, GROUP, 1, 1, 8>, 1, 1, 8};
+    if (tiles >= 384) return {w4_kernel<XT, GROUP, 1, 1, 4>, 1, 1, 4};
     return {w4_kernel<XT, GROUP, 1, 1, 16>, 1, 1, 16};
   }
   if (M <= 32) {
