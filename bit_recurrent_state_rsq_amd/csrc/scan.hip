@@ -291,14 +291,23 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     const size_t first = seg == 0 ? a.segs - 1 : 0;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) S[kt] = ws[first * slot + kt * kThreads];
+    // (the next segment's state is on its way while one is added)
+    f32x4 add[KT];
+    if (seg > 1)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) add[kt] = ws[slot + kt * kThreads];
     for (int j = 1; j < seg; ++j) {
       const float e = __builtin_amdgcn_exp2f(wd[j]);
+      f32x4 now[KT];
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const f32x4 t = ws[j * slot + kt * kThreads];
+      for (int kt = 0; kt < KT; ++kt) now[kt] = add[kt];
+      if (j + 1 < seg)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[kt][r] = __builtin_fmaf(S[kt][r], e, t[r]);
-      }
+        for (int kt = 0; kt < KT; ++kt) add[kt] = ws[(j + 1) * slot + kt * kThreads];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[kt][r] = __builtin_fmaf(S[kt][r], e, now[kt][r]);
     }
   }
 
@@ -686,9 +695,13 @@ struct ScanPlan {
 
 // Sequences are cut into segments that run side by side when heads and
 // sequences alone do not fill the chip: about kTarget workgroups (three for each
-// of 256 compute units) of equal length. Every segment but a sequence's last is
-// read twice (its state first), so one segment is kept where that fills it.
-constexpr int64_t kTarget = 768, kMinChunks = 4;
+// of 256 compute units, what fits at once) of equal length; 512 measured 273 us
+// and 1024 267 us where 768 take 220 (16384 tokens, 64 heads).
+// A segment costs its chunks one and a half times (the states first), and one
+// step for each segment before it, about 1/7 of a chunk's time: with n chunks,
+// sqrt(n / 11) of them a segment is the shortest that pays, and two chunks are
+// not worth a second pass.
+constexpr int64_t kTarget = 768;
 
 rsq_status plan_scan(const rsq_ssm* p, ScanPlan& w) {
   w.dkp = p->d_k <= 64 ? 64 : p->d_k <= 128 ? 128 : 256;
@@ -698,8 +711,8 @@ rsq_status plan_scan(const rsq_ssm* p, ScanPlan& w) {
   int64_t total = ceil_div(p->tokens, kL) + p->seqs;
   if (total > longest * p->seqs) total = longest * p->seqs;
   int64_t per = ceil_div(total * base, kTarget);
-  if (per < kMinChunks) per = kMinChunks;
-  if (per > longest) per = longest > 0 ? longest : 1;
+  while (per * per * 11 < longest) ++per;
+  if (per > longest || longest < 3) per = longest > 0 ? longest : 1;
   w.segs = (int)(longest > 0 ? ceil_div(longest, per) : 1);
   w.seg_chunks = (int)per;
   w.blocks = base * p->seqs * w.segs;
