@@ -171,7 +171,7 @@ void sequences(P& p, const at::Tensor& x, int inner, PyObject* offsets, PyObject
 }
 
 int32_t small(int64_t v, const char* what) {
-  if (v > 0x7fffffff) refuse(std::string(what) + " is too large");
+  if (v > 0x7fffffff || v < -0x7fffffff) refuse(std::string(what) + " is out of range");
   return (int32_t)v;
 }
 

@@ -222,8 +222,8 @@ extern "C" rsq_status rsq_rms_norm(const rsq_norm* p, void* stream) {
   if (!(p->eps >= 0.f) || p->eps > 3.4e38f) return fail(RSQ_E_INVALID, "eps must be finite and >= 0");
   if (p->group != 0 && (!codes || (p->group != 32 && p->group != 64 && p->group != 128) || p->cols % p->group))
     return fail(RSQ_E_INVALID, "group %d: 0, or 32, 64 or 128 dividing cols %d with an 8-bit output", p->group, p->cols);
+  if (p->rows == 0) return RSQ_OK;   // (an empty tensor has no address)
   if (codes != (p->scales != nullptr)) return fail(RSQ_E_INVALID, "scales are given with an 8-bit output, and only there");
-  if (p->rows == 0) return RSQ_OK;
   if (!p->x || !p->weight || !p->y) return fail(RSQ_E_INVALID, "x, weight and y must be non-NULL");
   if (p->x_stride < p->cols || p->y_stride < p->cols || (p->residual && p->residual_stride < p->cols))
     return fail(RSQ_E_INVALID, "a row stride is below %d columns", p->cols);

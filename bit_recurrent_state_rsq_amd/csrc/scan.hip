@@ -742,11 +742,11 @@ extern "C" rsq_status rsq_ssm_scan_workspace(const rsq_ssm* p, size_t* bytes) {
 extern "C" rsq_status rsq_ssm_scan(const rsq_ssm* p, void* stream) {
   if (const rsq_status s = check_ssm(p, true)) return s;
   if (!p->state) return fail(RSQ_E_INVALID, "state is NULL");
-  if (const rsq_status s = check_ssm_memory(p)) return s;
   const int64_t size = p->dtype == RSQ_BF16 ? 2 : 4;
   for (const int64_t stride : {p->x_stride, p->b_stride, p->c_stride, p->y_stride})
-    if (stride * size > kMaxRowBytes)
-      return fail(RSQ_E_UNSUPPORTED, "rows %lld bytes apart, more than 2^24", (long long)(stride * size));
+    if (stride > kMaxRowBytes / size)
+      return fail(RSQ_E_UNSUPPORTED, "rows %lld elements apart, more than 2^24 bytes", (long long)stride);
+  if (const rsq_status s = check_ssm_memory(p)) return s;
   ScanPlan w;
   if (const rsq_status s = plan_scan(p, w)) return s;
   if (w.bytes) {

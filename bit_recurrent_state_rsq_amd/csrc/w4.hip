@@ -2,7 +2,11 @@
 //   y[m, n] = sum_k x[m, k] code[n, k] scale[n, k / group]  (times x's own scales),
 // for the projections around a decode step.
 //
-// Half a byte a weight against 2 M operations: bound by memory at few rows.
+// Half a byte a weight against 2 M operations: bound by memory at few rows
+// (16 int8 rows x 28672 x 8192, 122 MB: 28.6 us, 4.3 TB/s, where a large copy
+// moves 4.7; 1 x 2048 x 4096 is 4.8 us of latency: launch, one round of loads, the
+// join), from 32 on by making bf16 numbers of the codes, which the vector unit
+// does for each 16 x MT rows anew (64 rows of bf16 76 us).
 // The packed layout holds 16 rows x 128 columns in 1 KB, 16 bytes a lane of a
 // wavefront's load: lane (g, n) has row n, and its word j the eight codes of
 // columns 32 j + 8 g .. + 7, which is what it feeds to the j-th product of 32
@@ -85,38 +89,47 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(PackArgs a) {
 
 constexpr int x_size(int xt) { return xt == kXF32 ? 4 : xt == kXBf16 ? 2 : 1; }
 
+// Memory from a scalar address on, with 32-bit offsets; `bytes` from it are in
+// range, where loads outside give zeros. The address is uniform over the workgroup.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  const uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+  const uint32_t high = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)high << 32 | low), 0,
+                                           __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+}
+constexpr int64_t kMaxRowBytes = 1 << 24;   // 32 rows of x then end below 2^30
+
 // Eight consecutive columns of a row of x for one product of 32 columns, as loaded.
 template <int XT>
 struct XRaw {
   static constexpr int kSize = x_size(XT), kWords = 2 * kSize;
   uint32_t w[kWords];
-  // zeros past the last row and column (K is a multiple of 32: a run of eight
-  // columns is inside or outside)
-  __device__ __forceinline__ void load(const W4Args& a, int64_t row, int64_t k, bool wide) {
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x) + (row * a.x_stride + k) * kSize;
+  __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0u;
-    if (row < a.M && k < a.K) {
-      if (wide) {
-        if constexpr (kSize == 1) {
-          const uint2 t = *reinterpret_cast<const uint2*>(p);
-          w[0] = t.x, w[1] = t.y;
-        } else {
-#pragma unroll
-          for (int i = 0; i < kSize / 2; ++i) {
-            const uint4 t = reinterpret_cast<const uint4*>(p)[i];
-            w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
-          }
-        }
-      } else if constexpr (kSize == 1) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
-      } else if constexpr (kSize == 2) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+  }
+  // at `offset` (the row's part of it checked against the buffer) + `column` bytes
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, uint32_t offset, uint32_t column, bool wide) {
+    if (wide) {
+      if constexpr (kSize == 1) {
+        const auto t = __builtin_amdgcn_raw_buffer_load_b64(x, (int)offset, (int)column, 0);
+        w[0] = t[0], w[1] = t[1];
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+        for (int i = 0; i < kSize / 2; ++i) {
+          const auto t = __builtin_amdgcn_raw_buffer_load_b128(x, (int)(offset + 16 * i), (int)column, 0);
+          w[4 * i] = t[0], w[4 * i + 1] = t[1], w[4 * i + 2] = t[2], w[4 * i + 3] = t[3];
+        }
+      }
+    } else {
+      zero();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int at = (int)(offset + e * kSize);
+        if constexpr (kSize == 1) w[e >> 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(x, at, (int)column, 0) << (8 * (e & 3));
+        else if constexpr (kSize == 2) w[e >> 1] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(x, at, (int)column, 0) << (16 * (e & 1));
+        else w[e] = __builtin_amdgcn_raw_buffer_load_b32(x, at, (int)column, 0);
       }
     }
   }
@@ -159,28 +172,24 @@ __device__ __forceinline__ void convert_x(const XRaw<XT>& r, XFrag<XT>& f) {
   }
 }
 
-// What a wavefront loads for a block of 128 columns: the codes and scales of NT
-// tiles and, when AHEAD, the first 16 rows of x.
-template <int XT, int GPB, int NT, bool AHEAD>
+// Codes and scales of NT tiles for a block of 128 columns, as loaded.
+template <int GPB, int NT>
 struct Block {
   u32x4 w[NT];
-  uint32_t s[NT][GPB];   // scales as stored
-  XRaw<XT> x[AHEAD ? 4 : 1];
-  __device__ __forceinline__ void load(const W4Args& a, int tile0, int kb, int64_t m0, int lane, bool wide) {
-    const int n16 = lane & 15, g = lane >> 4, tiles = a.npad >> 4;
+  uint32_t s[NT][GPB];
+  __device__ __forceinline__ void load(const W4Args& a, __amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales,
+                                       int tile0, int kb, int lane) {
+    const int tiles = a.npad >> 4, ssize = a.scale_f16 ? 2 : 4;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int t = tile0 + i < tiles ? tile0 + i : tiles - 1;   // a tile past the last is not stored
-      w[i] = *reinterpret_cast<const u32x4*>(a.codes + ((size_t)t * a.kblocks + kb) * 1024 + lane * 16);
+      const int t = min(i, tiles - 1 - tile0);   // a tile past the last is not stored
+      w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(codes, lane * 16, (t * a.kblocks + kb) * 1024, 0));
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
-        const size_t at = (size_t)(kb * GPB + q) * a.npad + 16 * t + n16;
-        s[i][q] = a.scale_f16 ? reinterpret_cast<const uint16_t*>(a.scales)[at] : reinterpret_cast<const uint32_t*>(a.scales)[at];
+        const int row = (int)(((uint32_t)(kb * GPB + q) * (uint32_t)a.npad + 16 * t) * ssize);
+        s[i][q] = a.scale_f16 ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(scales, (lane & 15) * 2, row, 0)
+                              : (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(scales, (lane & 15) * 4, row, 0);
       }
-    }
-    if constexpr (AHEAD) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j].load(a, m0 + n16, (int64_t)kb * 128 + 32 * j + 8 * g, wide);
     }
   }
   __device__ __forceinline__ float scale(const W4Args& a, int i, int q) const {
@@ -203,11 +212,10 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
   extern __shared__ float part[];   // [WAVES][MT * 16][NT * 16]
   constexpr int GPB = 128 / GROUP, SPG = GROUP / 32;   // groups of a block, products of a group
   constexpr bool INT = XT == kXInt8;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, g = lane >> 4;
   const int tile0 = blockIdx.x * NT;
   const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-  constexpr bool AHEAD = MT == 1;
   const bool wide = a.x_stride * x_size(XT) % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
 
   f32x4 y[NT][MT];
@@ -216,11 +224,32 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) y[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  Block<XT, GPB, NT, AHEAD> next;
-  if (wave < a.kblocks) next.load(a, tile0, wave, m0, lane, wide);
+  constexpr int size = x_size(XT);
+  const int xrow = (int)(a.x_stride * size);
+  const int rows = min(a.M - (int)m0, 16 * MT);
+  const auto rx = buffer(reinterpret_cast<const uint8_t*>(a.x) + m0 * (int64_t)xrow, (uint32_t)(rows * xrow));
+  const auto rw = buffer(a.codes + (size_t)tile0 * a.kblocks * 1024, 0xFFFFFFFFu);
+  const auto rs = buffer(reinterpret_cast<const uint8_t*>(a.scales) + (size_t)tile0 * 16 * (a.scale_f16 ? 2 : 4), 0xFFFFFFFFu);
+  const uint32_t xoff = (uint32_t)(n16 * xrow + 8 * g * size);
+  // the next block's codes, and the next 16 rows of x, are on their way while
+  // the last ones are worked on
+  Block<GPB, NT> next;
+  XRaw<XT> xnext[4];
+  auto load_x = [&](int kb, int m) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // (K is a multiple of 32: a product's columns are all inside or all outside)
+      if (kb * 128 + 32 * j < a.K) xnext[j].load(rx, xoff + (uint32_t)(16 * m * xrow), (uint32_t)((kb * 128 + 32 * j) * size), wide);
+      else xnext[j].zero();
+    }
+  };
+  if (wave < a.kblocks) {
+    next.load(a, rw, rs, tile0, wave, lane);
+    load_x(wave, 0);
+  }
   for (int kb = wave; kb < a.kblocks; kb += WAVES) {
-    const Block<XT, GPB, NT, AHEAD> b = next;
-    if (kb + WAVES < a.kblocks) next.load(a, tile0, kb + WAVES, m0, lane, wide);
+    const Block<GPB, NT> b = next;
+    if (kb + WAVES < a.kblocks) next.load(a, rw, rs, tile0, kb + WAVES, lane);
     const auto& w = b.w;
     float s[NT][GPB];
 #pragma unroll
@@ -231,15 +260,9 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
     for (int m = 0; m < MT; ++m) {
       XFrag<XT> x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (AHEAD) {
-          convert_x(b.x[j], x[j]);
-        } else {
-          XRaw<XT> r;
-          r.load(a, m0 + 16 * m + n16, (int64_t)kb * 128 + 32 * j + 8 * g, wide);
-          convert_x(r, x[j]);
-        }
-      }
+      for (int j = 0; j < 4; ++j) convert_x(xnext[j], x[j]);
+      if (m + 1 < MT) load_x(kb, m + 1);
+      else if (kb + WAVES < a.kblocks) load_x(kb + WAVES, 0);
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
         // scales of this lane's four rows of x in this group
@@ -297,6 +320,9 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
             for (int r = 0; r < 4; ++r) y[i][m][r] = __builtin_fmaf(acc[r], s[i][q] * xs[r], y[i][m][r]);
           }
         }
+        // (groups one after another: mixed, they hold registers that cost more in
+        // resident wavefronts than their order gains)
+        if constexpr (MT > 1) __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -329,20 +355,30 @@ struct W4Pick {
   int nt, mt, waves;
 };
 
+// Workgroups of NT tiles of weight rows and MT of 16 rows of x. More tiles read
+// and convert x fewer times (N / (16 NT)) and the weights fewer times (M / (16 MT),
+// all but the first from L2); fewer tiles and more wavefronts put more of the
+// chip to work where there are few. By the number of 16 x 16 tiles of y, in us at
+// bf16 rows (M x N x K), the shape taken first:
+//   below 384    one tile:  1 x 2048 x 4096 4.2, two tiles 5.1, four 6.9
+//   to 512       two:       64 x 2048 x 4096 6.7, one 10.3, four 8.1
+//   to 1280      four:      16 x 8512 x 2048 5.9, two 6.6, one 8.0; 64 x 4096 x 4096 10.8, two 13.3
+//   above        four, four wavefronts: 33 x 8512 x 2048 9.5, eight 10.9; 16 x 28672 x 8192 31.6, 33.9
+// There 32 rows of x, 64 and more go two times 16 a workgroup: 32 x 28672 x 8192
+// 44, once 16 56; 64 rows 76, 88 (four times 16: 100). Not fp32 rows, whose pieces
+// then leave one wavefront a SIMD (64 rows 177, once 16 146), nor bf16 and E4M3
+// in groups of 32, which keep a start for every group (256 x 4096 x 4096 above
+// 40, once 16 35).
 template <int XT, int GROUP>
 W4Pick pick_shape(int M, int tiles) {
-  // few weight rows: more wavefronts share a tile's columns
-  if (M <= 16) {
-    if (tiles >= 1024) return {w4_kernel<XT, GROUP, 4, 1, 8>, 4, 1, 8};
-    if (tiles >= 384) return {w4_kernel<XT, GROUP, 1, 1, 4>, 1, 1, 4};
-    return {w4_kernel<XT, GROUP, 1, 1, 16>, 1, 1, 16};
-  }
-  if (M <= 32) {
-    if (tiles >= 1024) return {w4_kernel<XT, GROUP, 2, 2, 4>, 2, 2, 4};
-    return {w4_kernel<XT, GROUP, 1, 2, 8>, 1, 2, 8};
-  }
-  if (tiles >= 1024) return {w4_kernel<XT, GROUP, 2, 4, 4>, 2, 4, 4};
-  return {w4_kernel<XT, GROUP, 1, 4, 8>, 1, 4, 8};
+  const int64_t mtiles = ceil_div(M, 16), work = tiles * mtiles;
+  constexpr int kMost = XT == kXF32 ? 8 : 16;   // (fp32 rows need more registers than sixteen wavefronts leave)
+  if (work < 384) return {w4_kernel<XT, GROUP, 1, 1, kMost>, 1, 1, kMost};
+  if (work <= 512) return {w4_kernel<XT, GROUP, 2, 1, 8>, 2, 1, 8};
+  if (work < 1280) return {w4_kernel<XT, GROUP, 4, 1, 8>, 4, 1, 8};
+  constexpr int kRows = XT == kXF32 || (XT != kXInt8 && GROUP == 32) ? 1 : 2;
+  if (mtiles == 2 || mtiles >= 4) return {w4_kernel<XT, GROUP, 4, kRows, 4>, 4, kRows, 4};
+  return {w4_kernel<XT, GROUP, 4, 1, 4>, 4, 1, 4};
 }
 
 template <int XT>
@@ -364,9 +400,12 @@ rsq_status w4_layout(int32_t n, int32_t k, int32_t group, int32_t scale_dtype, W
   if (group != 32 && group != 64 && group != 128) return fail(RSQ_E_INVALID, "group %d not in {32, 64, 128}", group);
   if (k % group) return fail(RSQ_E_INVALID, "group %d does not divide k %d", group, k);
   if (scale_dtype != RSQ_F32 && scale_dtype != RSQ_F16) return fail(RSQ_E_INVALID, "scale_dtype %d", scale_dtype);
-  if (n > (1 << 26) || k > (1 << 26)) return fail(RSQ_E_UNSUPPORTED, "n %d, k %d above 2^26", n, k);
+  // (a workgroup reaches its tiles' codes, and all groups' scales, by 31-bit offsets)
+  if (n > (1 << 26) || k > (1 << 22)) return fail(RSQ_E_UNSUPPORTED, "n %d, k %d: above 2^26 or 2^22", n, k);
   l.kblocks = (k + 127) / 128;
   l.npad = (n + 15) / 16 * 16;
+  if ((int64_t)l.npad * l.kblocks * 128 > ((int64_t)1 << 34) - 4096)
+    return fail(RSQ_E_UNSUPPORTED, "n %d, k %d: 2^34 weights and more", n, k);
   l.codes = (size_t)l.npad * l.kblocks * 64;
   l.total = l.codes + (size_t)l.npad * l.kblocks * (128 / group) * (scale_dtype == RSQ_F16 ? 2 : 4);
   return RSQ_OK;
@@ -416,12 +455,14 @@ extern "C" rsq_status rsq_w4_linear(const rsq_w4* p, void* stream) {
     default: return fail(RSQ_E_INVALID, "x_dtype %d", p->x_dtype);
   }
   if (p->out_dtype != RSQ_F32 && p->out_dtype != RSQ_BF16) return fail(RSQ_E_INVALID, "out_dtype %d", p->out_dtype);
-  if ((size == 1) != (p->x_scale != nullptr)) return fail(RSQ_E_INVALID, "x_scale is given with 8-bit x, and only there");
   if (p->x_group != 0 && (size != 1 || p->x_group != p->group))
     return fail(RSQ_E_INVALID, "x_group %d: 0, or with 8-bit x the weights' group %d", p->x_group, p->group);
   if (p->m < 0 || p->m > 65535 * 16) return fail(RSQ_E_INVALID, "m %d not in [0, %d]", p->m, 65535 * 16);
-  if (p->m == 0) return RSQ_OK;
+  if (p->m == 0) return RSQ_OK;   // (an empty tensor has no address)
+  if ((size == 1) != (p->x_scale != nullptr)) return fail(RSQ_E_INVALID, "x_scale is given with 8-bit x, and only there");
   if (!p->x || !p->packed || !p->y) return fail(RSQ_E_INVALID, "x, packed and y must be non-NULL");
+  if (p->x_stride > kMaxRowBytes / size)
+    return fail(RSQ_E_UNSUPPORTED, "rows of x %lld elements apart, more than 2^24 bytes", (long long)p->x_stride);
   if (p->x_stride < p->k || p->y_stride < p->n) return fail(RSQ_E_INVALID, "a row stride is shorter than its row");
   const int osize = p->out_dtype == RSQ_BF16 ? 2 : 4;
   if (!aligned(p->x, size) || !aligned(p->y, osize) || !aligned(p->x_scale, 4) || !aligned(p->packed, 16))

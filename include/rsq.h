@@ -329,7 +329,8 @@ rsq_status rsq_allocate_head_bits(const float* decay_sq, const float* range, int
  * max_len. Empty sequences are allowed. Offsets live on the device, so they are
  * not checked on the host: the kernels clamp them into [0, tokens], and of a
  * sequence longer than max_len only its first max_len rows are taken. Rows of y
- * that belong to no sequence are left as they were.
+ * that belong to no sequence are left as they were; what a row of two sequences
+ * gets is one of their two results.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -377,7 +378,8 @@ rsq_status rsq_causal_conv(const rsq_conv* conv, void* stream);
  *              be NULL when that is 0). Its contents need not be kept.
  * x, B, C, y and state are 16-byte aligned, the strides of x, B, C and y
  * multiples of 16 bytes; d_k and d_v are multiples of 8.
- * rsq_ssm_scan takes d_k <= 256 (bf16) or 128 (fp32). bf16: products take bf16
+ * rsq_ssm_scan takes d_k <= 256 (bf16) or 128 (fp32), d_v <= 4096 and rows of x,
+ * B, C and y at most 2^24 bytes apart (RSQ_E_UNSUPPORTED beyond). bf16: products take bf16
  * factors (S and the token weights are rounded to bf16 where they enter y; the
  * state itself is exact to fp32). An infinite or NaN x makes its column NaN
  * from its token on; earlier tokens are not touched.
@@ -468,9 +470,11 @@ rsq_status rsq_rms_norm(const rsq_norm* norm, void* stream);
  *   x_scale      device fp32 [m] (x_group 0) or [m][k / group] (x_group = group);
  *                NULL without 8-bit x
  *   out_dtype    RSQ_F32 | RSQ_BF16
- * Sums are fp32 (int8: int32 inside a group). Meant for few rows: every 16 to 64
+ * Sums are fp32 (int8: int32 inside a group). Meant for few rows: every 16 or 32
  * rows of x read the weights once. fp32 and bf16 x may reach 2^100 (beyond, the
- * offset that codes carry inside may overflow).
+ * offset that codes carry inside may overflow). n up to 2^26, k to 2^22, below
+ * 2^34 weights (with the padding), rows of x at most 2^24 bytes apart
+ * (RSQ_E_UNSUPPORTED beyond).
  */
 rsq_status rsq_w4_bytes(int32_t n, int32_t k, int32_t group, int32_t scale_dtype, size_t* bytes);
 rsq_status rsq_w4_pack(const int8_t* codes, const void* scales, int32_t n, int32_t k, int32_t group,

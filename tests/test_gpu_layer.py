@@ -306,6 +306,52 @@ def test_scan_is_repeatable():
         assert torch.equal(y, y0) and torch.equal(S, S0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_far_apart(dtype):
+    """Rows 2^24 bytes apart, the most the scan takes: 150 of them pass 2^31 bytes (two chunks, several bases)."""
+    n, cols = 150, (1 << 24) // torch.finfo(dtype).bits * 8
+    case = ssm_case(n, 2, 1, 64, 64, dtype, slices=False)
+    far = torch.empty(n, cols, dtype=dtype, device="cuda")
+    far[:, :128], far[:, 256: 320], far[:, 512: 576] = case[0].view(n, 128), case[3][:, 0], case[4][:, 0]
+    x, B, C = far[:, :128].view(n, 2, 64), far[:, 256: 320].view(n, 1, 64), far[:, 512: 576].view(n, 1, 64)
+    off = torch.tensor([0, 3, n], dtype=torch.int32).cuda()
+    want = rsq.ssm_scan(*case[:5], offsets=off, max_len=n - 3)
+    out = torch.empty(n, cols, dtype=dtype, device="cuda")[:, :128].view(n, 2, 64)
+    y, S = rsq.ssm_scan(x, case[1], case[2], B, C, offsets=off, max_len=n - 3, out=out)
+    assert torch.equal(y, want[0]) and torch.equal(S, want[1])
+    w = gen(4)(128, 4)
+    z = rsq.causal_conv(far[:, :128], w, offsets=off, max_len=n - 3, out=out.view(n, 128))
+    assert torch.equal(z, rsq.causal_conv(case[0].reshape(n, 128), w, offsets=off, max_len=n - 3))
+
+
+def test_nothing_to_do():
+    """No tokens, no rows: outputs are empty, states as they were, a new scan state zero."""
+    e = lambda *s: torch.zeros(*s, dtype=BF16, device="cuda")   # noqa: E731
+    A, w = -torch.ones(2, device="cuda"), torch.ones(8, 4, device="cuda")
+    cs = gen(1)(3, 8, 3, dtype=BF16)
+    for x, off in ((e(3, 0, 8), None), (e(0, 8), torch.zeros(4, dtype=torch.int32, device="cuda")),
+                   (e(5, 8), torch.full((4,), 2, dtype=torch.int32, device="cuda"))):
+        st = cs.clone()
+        y = rsq.causal_conv(x, w, state=st, offsets=off, max_len=0 if off is not None else None)
+        assert y.shape == x.shape and torch.equal(st, cs)
+    given = gen(2)(3, 2, 8, 16)
+    for lead, off in (((3, 0), None), ((0,), torch.zeros(4, dtype=torch.int32, device="cuda")),
+                      ((5,), torch.full((4,), 2, dtype=torch.int32, device="cuda"))):
+        args = e(*lead, 2, 16), e(*lead, 2), A, e(*lead, 1, 8), e(*lead, 1, 8)
+        kw = dict(offsets=off, max_len=0 if off is not None else None)
+        y, S = rsq.ssm_scan(*args, **kw)
+        assert y.shape == args[0].shape and S.shape == (3, 2, 8, 16) and (S == 0).all()
+        st = given.clone()
+        y, S = rsq.ssm_scan(*args, state=st, **kw)
+        assert S is st and torch.equal(st, given)
+    assert rsq.rms_norm(e(0, 64), torch.ones(64, device="cuda")).shape == (0, 64)
+    q, sc = rsq.rms_norm(e(2, 0, 64), torch.ones(64, device="cuda"), out_dtype="int8", group=32)
+    assert q.shape == (2, 0, 64) and sc.shape == (2, 0, 2)
+    w4 = rsq.W4Weight(torch.ones(16, 64, dtype=torch.int8, device="cuda"), torch.ones(16, 2, device="cuda"))
+    assert rsq.w4_linear(e(0, 64), w4).shape == (0, 16) and rsq.w4_linear(e(2, 0, 64), w4).shape == (2, 0, 16)
+    assert rsq.w4_linear(q, w4, x_scale=sc).shape == (2, 0, 16)
+
+
 def test_scan_offsets_out_of_range_are_clamped():
     case = ssm_case(60, 2, 1, 64, 64, BF16)
     off = torch.tensor([0, 20, 15, 1000], dtype=torch.int32).cuda()
@@ -485,6 +531,44 @@ def test_w4(xt, m, n, k, group):
     for out in ("f32", "bf16"):
         want, bound = w4_reference(codes, s, x, xs, group, out)
         check(rsq.w4_linear(x, w, x_scale=xs, out_dtype=out), want, bound, out)
+
+
+@pytest.mark.parametrize("xt", [BF16, F32, "int8g", "e4m3"])
+@pytest.mark.parametrize("m,n,k,group", [(60, 1990, 384, 64), (30, 6100, 160, 32), (40, 6100, 256, 128), (33, 8003, 96, 32),
+                                         (17, 12820, 160, 32), (5, 20500, 192, 64), (70, 5500, 192, 64), (90, 5500, 96, 32)])
+def test_w4_more_rows(xt, m, n, k, group):
+    """Several tiles of weight rows and of x a workgroup, the last ones cut."""
+    codes, s, x, xs = w4_case(m, n, k, group, xt, torch.float16, seed=m)
+    w = rsq.W4Weight(codes, s)
+    want, bound = w4_reference(codes, s, x, xs, group, "f32")
+    out = torch.full((m + 1, n + 1), 3.0, device="cuda")
+    check(rsq.w4_linear(x, w, x_scale=xs, out_dtype="f32", out=out[:m, :n]), want, bound)
+    assert (out[m] == 3).all() and (out[:, n] == 3).all()
+
+
+@pytest.mark.parametrize("scales", [F32, torch.float16])
+def test_w4_large_weights(scales):
+    """Packed codes of more than 2^32 bytes: the last rows are right, and the first."""
+    n, k, group = (1 << 18) + 3, 1 << 15, 32
+    codes = torch.zeros(n, k, dtype=torch.int8, device="cuda")
+    s = torch.zeros(n, k // group, dtype=scales, device="cuda")
+    some = torch.tensor([0, 1, 17, n // 2, n - 20, n - 1], device="cuda")
+    c0, s0, x, _ = w4_case(3, 6, k, group, BF16, scales)
+    codes[some], s[some] = c0, s0
+    y = rsq.w4_linear(x, rsq.W4Weight(codes, s), out_dtype="f32")
+    want, bound = w4_reference(c0, s0, x, None, group, "f32")
+    check(y[:, some], want, bound)
+    y[:, some] = 0
+    assert (y == 0).all()
+
+
+def test_w4_rows_far_apart():
+    """Rows of x 2^24 bytes apart, the most there is."""
+    codes, s, x, _ = w4_case(40, 40, 192, 64, BF16, torch.float16)
+    far = torch.empty(40, 1 << 23, dtype=BF16, device="cuda")
+    far[:, 5:197] = x
+    w = rsq.W4Weight(codes, s)
+    assert torch.equal(rsq.w4_linear(far[:, 5:197], w), rsq.w4_linear(x, w))
 
 
 @pytest.mark.parametrize("xt", [BF16, F32, "int8", "e4m3"])
@@ -828,3 +912,42 @@ def test_calls_on_a_stream_of_their_own():
     for y, S in got:
         assert same(y, want[0]) and same(S, want[1])
     assert torch.equal(c, rsq.causal_conv(x[None], w, b))
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls that run side by side, from two threads: workspaces, staging and errors are each call's own."""
+    import threading
+
+    r = gen(12)
+    x, w = r(32, 1024, dtype=BF16), torch.ones(1024, device="cuda")
+    codes, s, _, _ = w4_case(1, 2048, 1024, 64, BF16, torch.float16)
+    w4 = rsq.W4Weight(codes, s)
+    cases = [ssm_case(2100, 2, 1, 64, 64, BF16, seed=i) for i in range(2)]
+    args = [[t[None] for t in c[:2]] + [c[2]] + [t[None] for t in c[3:5]] for c in cases]
+
+    def calls(i, stream=None):
+        q, sc = rsq.rms_norm(x, w, out_dtype="int8", stream=stream)
+        return [rsq.w4_linear(q, w4, x_scale=sc, stream=stream), *rsq.ssm_scan(*args[i], stream=stream)]
+
+    want = [calls(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, got, wrong = [torch.cuda.Stream() for _ in range(2)], [None, None], []
+
+    def work(i):
+        try:
+            for _ in range(20):
+                got[i] = calls(i, streams[i])
+                with pytest.raises(ValueError):
+                    rsq.rms_norm(x, w[:-1], stream=streams[i])
+            streams[i].synchronize()
+        except Exception as e:  # a failure of a thread is the test's
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    for i in range(2):
+        assert all(same(a, b) for a, b in zip(got[i], want[i]))

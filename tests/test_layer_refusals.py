@@ -89,6 +89,8 @@ SSM = dict(dtype=_abi.BF16, seqs=2, heads=8, groups=2, d_k=128, d_v=64, softplus
     (dict(max_len=9), INVALID),
     (dict(x_stride=504), INVALID),
     (dict(x_stride=516), INVALID),                     # not a multiple of 16 bytes
+    (dict(x_stride=(1 << 23) + 8), UNSUPPORTED),       # rows above 2^24 bytes apart
+    (dict(y_stride=(1 << 62) + 8), UNSUPPORTED),
     (dict(b_stride=260), INVALID),
     (dict(y_stride=514), INVALID),
     (dict(dt_stride=7), INVALID),
@@ -192,6 +194,13 @@ def test_w4_bytes_refusals(n, k, group):
     assert w4_bytes(n, k, group)[0] == INVALID
 
 
+@pytest.mark.parametrize("n,k,group", [((1 << 26) + 1, 32, 32), (16, (1 << 22) + 32, 32), (1 << 26, 256, 32),
+                                       (1 << 25, 512 + 32, 32), (0x7FFFFFFF, 32, 32)])
+def test_w4_bytes_limits(n, k, group):
+    assert w4_bytes(n, k, group)[0] == UNSUPPORTED
+    assert w4_bytes(1 << 26, 96, group)[0] == 0 and w4_bytes(16, 1 << 22, group)[0] == 0
+
+
 W4 = dict(x_dtype=_abi.INT8, out_dtype=_abi.BF16, m=4, n=64, k=256, group=64, scale_dtype=_abi.F16, x_group=0,
           x=addr(0), x_stride=256, x_scale=addr(1), packed=addr(2), packed_bytes=1 << 20, y=addr(3), y_stride=64)
 
@@ -211,6 +220,9 @@ W4 = dict(x_dtype=_abi.INT8, out_dtype=_abi.BF16, m=4, n=64, k=256, group=64, sc
     (dict(packed_bytes=64), BUFFER),
     (dict(x_stride=255), INVALID),
     (dict(y_stride=63), INVALID),
+    (dict(x_stride=(1 << 24) + 1), UNSUPPORTED),
+    (dict(x_stride=1 << 63 - 1), UNSUPPORTED),
+    (dict(m=65535 * 16 + 1), INVALID),
     (dict(y=addr(0)), INVALID),
     (dict(y=addr(2)), INVALID),
 ])
@@ -260,6 +272,7 @@ def z(*shape, dtype=torch.float32):
     lambda: rsq.rms_norm(z(8), z(8)),
     lambda: rsq.rms_norm(z(2, 8), z(8), out_dtype="fp4"),
     lambda: rsq.rms_norm(z(2, 8), None),
+    lambda: rsq.rms_norm(z(2, 64), z(64), out_dtype="int8", group=(1 << 32) + 64),
     lambda: rsq.rms_norm(z(2, 8), z(8), residual=z(2, 7)),
     lambda: rsq.W4Weight(z(16, 128), z(16, 1)),
     lambda: rsq.W4Weight(z(16, 128, dtype=torch.int8), z(15, 1)),
