@@ -66,7 +66,10 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[N]) {
 
 // A chunk's rows as a buffer: one scalar base, 32-bit offsets, and rows past the
 // sequence's end out of its range, where loads give zeros and stores are dropped.
-// A chunk that is asked for has a row (t0 < len). Offsets of lanes without a row or column of their own start at kOutside.
+// Offsets of lanes without a row or column of their own start at kOutside. All of
+// a loop's loads are unconditional (a chunk past the end has no rows): behind a
+// branch the compiler could not tell how many are on their way, and would wait
+// for the next chunk's to use this one's.
 constexpr uint32_t kOutside = 0x80000000u;
 constexpr int64_t kMaxRowBytes = 1 << 24;   // a chunk then ends below 2^30, and nothing wraps
 struct Rows {
@@ -78,7 +81,7 @@ struct Rows {
     const uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
     const uint32_t high = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
     const uint64_t u = (uint64_t)high << 32 | low;
-    const int rows = min(len - t0, kL);   // t0 < len
+    const int rows = max(min(len - t0, kL), 0);
     rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0,
                                              __builtin_amdgcn_readfirstlane((int)(rows * row_bytes)), 0x00020000);
   }
@@ -319,6 +322,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   const int crow = (int)(a.s.c_stride * sizeof(T)), yrow = (int)(a.s.y_stride * sizeof(T));
   const float A2 = a.s.A[h] * 1.44269504088896f;   // decays in powers of two
   const float Dh = a.s.D ? a.s.D[h] : 0.f;
+  const float dt_bias = a.s.dt_bias ? a.s.dt_bias[h] : 0.f;
 
   // ---- a chunk's rows: B and x go through registers to LDS one chunk ahead,
   // C's rows 16 wave .. are fragments as they are
@@ -328,8 +332,10 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   const int bk = (tid % (DK / 8)) * 8, xv8 = (tid % (kV / 8)) * 8;
   uint32_t boff = bk < dk ? (uint32_t)(tid / (DK / 8) * brow + bk * (int)sizeof(T)) : kOutside;
   uint32_t xoff = v0 + xv8 < dv ? (uint32_t)(tid / (kV / 8) * xrow + xv8 * (int)sizeof(T)) : kOutside;
+  const int c_end = min(chunks, (seg + 1) * a.seg_chunks);
+  const int end = min(len, c_end * kL);   // (int: c_end * kL is below len + kL)
   auto load_bx = [&](int t0) {
-    const Rows rB(Bp, brow, t0, len), rX(x, xrow, t0, len);
+    const Rows rB(Bp, brow, t0, end), rX(x, xrow, t0, end);
 #pragma unroll
     for (int i = 0; i < NB; ++i) rb[i].load(rB, boff + (uint32_t)(i * RB * brow));
 #pragma unroll
@@ -337,7 +343,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   };
   uint32_t coff = (uint32_t)((16 * wave + n16) * crow + 8 * g * (int)sizeof(T));
   auto load_c = [&](int t0) {
-    const Rows rC(Cp, crow, t0, len);
+    const Rows rC(Cp, crow, t0, end);
 #pragma unroll
     for (int i = 0; i < (STATES ? 0 : KS); ++i) {
       uint32_t at = coff + (uint32_t)(32 * i * sizeof(T));
@@ -359,7 +365,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   auto decays = [&](float dt, int t0, int par) {
     float delta = 0.f;
     if (t0 + lane < len) {
-      delta = a.s.dt_bias ? dt + a.s.dt_bias[h] : dt;
+      delta = dt + dt_bias;
       if (a.s.softplus) delta = softplus(delta);
     }
     // a token that decays by 2^-2000 keeps nothing of an fp32 state
@@ -387,18 +393,21 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     }
   };
   const T* dtp = reinterpret_cast<const T*>(a.s.dt) + begin * a.s.dt_stride + h;
-  auto load_dt = [&](int t0) { return t0 + lane < len ? to_f32(dtp[(int64_t)(t0 + lane) * a.s.dt_stride]) : 0.f; };
+  const int dtrow = (int)(a.s.dt_stride * sizeof(T));
+  auto load_dt = [&](int t0) {
+    const Rows r(dtp, dtrow, t0, end);
+    if constexpr (PI == 1) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r.rsrc, lane * dtrow, 0, 0) << 16;
+    else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r.rsrc, lane * dtrow, 0, 0);
+  };
 
-  const int c_end = min(chunks, (seg + 1) * a.seg_chunks);
   int c = seg * a.seg_chunks;
-  float dt_next = 0.f;   // of wavefront 0: dt of the chunk after this one
+  uint32_t dt_next = 0u;   // dt of the chunk after this one (of use to wavefront 0)
   if (c < c_end) {
+    const uint32_t dt = load_dt(c * kL);
+    dt_next = load_dt((c + 1) * kL);
     load_bx(c * kL);
     load_c(c * kL);
-    if (wave == 0) {
-      dt_next = load_dt((c + 1) * kL);
-      decays(load_dt(c * kL), c * kL, c & 1);
-    }
+    if (wave == 0) decays(__uint_as_float(dt), c * kL, c & 1);
   }
   if (tid < 2 * kV) lds_first[tid / kV][tid % kV] = kL;
   if (tid < 2) lds_bad[tid] = 0;
@@ -460,16 +469,10 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     __syncthreads();
     const bool bad = __builtin_amdgcn_readfirstlane(lds_bad[par]) != 0;
     const bool more = c + 1 < c_end;
-    if (more) {
-      if (wave == 0) {
-        const float dt = dt_next;
-        dt_next = load_dt(t0 + 2 * kL);
-        load_bx(t0 + kL);
-        decays(dt, t0 + kL, par ^ 1);
-      } else {
-        load_bx(t0 + kL);
-      }
-    }
+    const uint32_t dt = dt_next;
+    dt_next = load_dt(t0 + 2 * kL);
+    load_bx(t0 + kL);
+    if (wave == 0 && more) decays(__uint_as_float(dt), t0 + kL, par ^ 1);
     if (tid < kV) lds_first[par ^ 1][tid] = kL;
     if (tid == kV) lds_bad[par ^ 1] = 0;
 
@@ -593,7 +596,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (more) load_c(t0 + kL);
+      load_c(t0 + kL);
     }
 
     // ---- S <- decay S + B^T (w x)
@@ -602,6 +605,15 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[kt][r] *= decay;
+    // Two tiles of keys side by side; the next two are read while they are worked on.
+    constexpr int STEPS = KT / 2 * PI;
+    u32x4 bf[2][2];
+    auto read_b = [&](int ts, int step, u32x4 (&out)[2]) {
+      const int k2 = step / PI * 2, p = step % PI;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) out[e] = read_tr8<DK>(lds_b + p * BB + 32 * ts * TB::kBytes + (a_btr ^ ((k2 + e) << 5)));
+    };
+    read_b(0, 0, bf[0]);
 #pragma unroll
     for (int ts = 0; ts < kL / 32; ++ts) {
       u32x4 xr[PI];
@@ -622,20 +634,17 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
 #pragma unroll
         for (int q = 0; q < PW; ++q) xw[q][i] = p3[q];
       }
-      // four tiles of keys side by side
 #pragma unroll
-      for (int k4 = 0; k4 < KT; k4 += 4) {
+      for (int step = 0; step < STEPS; ++step) {
+        const int now = (ts * STEPS + step) & 1;
+        if (step + 1 < STEPS) read_b(ts, step + 1, bf[now ^ 1]);
+        else if (ts + 1 < kL / 32) read_b(ts + 1, 0, bf[now ^ 1]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int p = 0; p < PI; ++p) {
-          u32x4 bf[4];
+        for (int q = 0; q < PW; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) bf[e] = read_tr8<DK>(lds_b + p * BB + 32 * ts * TB::kBytes + (a_btr ^ ((k4 + e) << 5)));
-#pragma unroll
-          for (int q = 0; q < PW; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (p + q < 3) S[k4 + e] = mfma(bf[e], xw[q], S[k4 + e]);
-        }
+          for (int e = 0; e < 2; ++e)
+            if (step % PI + q < 3) S[step / PI * 2 + e] = mfma(bf[now][e], xw[q], S[step / PI * 2 + e]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -743,7 +752,9 @@ extern "C" rsq_status rsq_ssm_scan(const rsq_ssm* p, void* stream) {
   if (const rsq_status s = check_ssm(p, true)) return s;
   if (!p->state) return fail(RSQ_E_INVALID, "state is NULL");
   const int64_t size = p->dtype == RSQ_BF16 ? 2 : 4;
-  for (const int64_t stride : {p->x_stride, p->b_stride, p->c_stride, p->y_stride})
+  // (the kernel counts rows in int, some chunks ahead of the last)
+  if (p->max_len > 0x7fffffff - 4096) return fail(RSQ_E_UNSUPPORTED, "max_len %lld", (long long)p->max_len);
+  for (const int64_t stride : {p->x_stride, p->b_stride, p->c_stride, p->dt_stride, p->y_stride})
     if (stride > kMaxRowBytes / size)
       return fail(RSQ_E_UNSUPPORTED, "rows %lld elements apart, more than 2^24 bytes", (long long)stride);
   if (const rsq_status s = check_ssm_memory(p)) return s;

@@ -378,8 +378,8 @@ rsq_status rsq_causal_conv(const rsq_conv* conv, void* stream);
  *              be NULL when that is 0). Its contents need not be kept.
  * x, B, C, y and state are 16-byte aligned, the strides of x, B, C and y
  * multiples of 16 bytes; d_k and d_v are multiples of 8.
- * rsq_ssm_scan takes d_k <= 256 (bf16) or 128 (fp32), d_v <= 4096 and rows of x,
- * B, C and y at most 2^24 bytes apart (RSQ_E_UNSUPPORTED beyond). bf16: products take bf16
+ * rsq_ssm_scan takes d_k <= 256 (bf16) or 128 (fp32), d_v <= 4096, max_len
+ * below 2^31 - 4096 and rows at most 2^24 bytes apart (RSQ_E_UNSUPPORTED beyond). bf16: products take bf16
  * factors (S and the token weights are rounded to bf16 where they enter y; the
  * state itself is exact to fp32). An infinite or NaN x makes its column NaN
  * from its token on; earlier tokens are not touched.

@@ -91,6 +91,8 @@ SSM = dict(dtype=_abi.BF16, seqs=2, heads=8, groups=2, d_k=128, d_v=64, softplus
     (dict(x_stride=516), INVALID),                     # not a multiple of 16 bytes
     (dict(x_stride=(1 << 23) + 8), UNSUPPORTED),       # rows above 2^24 bytes apart
     (dict(y_stride=(1 << 62) + 8), UNSUPPORTED),
+    (dict(dt_stride=(1 << 23) + 1), UNSUPPORTED),
+    (dict(tokens=0x7FFFFFFF, max_len=0x7FFFF001, offsets=addr(9)), UNSUPPORTED),
     (dict(b_stride=260), INVALID),
     (dict(y_stride=514), INVALID),
     (dict(dt_stride=7), INVALID),
