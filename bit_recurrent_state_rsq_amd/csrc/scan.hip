@@ -534,9 +534,9 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
       const float before = __builtin_amdgcn_ldexpf(1.f, power);
 #pragma unroll
       for (int vp = 0; vp < kV / 16; vp += VN) {
-        f32x4 acc[VN];
+        f32x4 acc[VN], px[VN];   // S^T C and P X apart: shorter chains of dependent products
 #pragma unroll
-        for (int e = 0; e < VN; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int e = 0; e < VN; ++e) acc[e] = px[e] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -549,10 +549,6 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
                 if (p + q < 3) acc[e] = mfma(sf, cf[i][q], acc[e]);
             }
 #pragma unroll
-        for (int e = 0; e < VN; ++e)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[e][r] *= before;
-#pragma unroll
         for (int j2 = 0; j2 < kL / 32; ++j2) {
           if (2 * j2 <= wave) {
 #pragma unroll
@@ -562,11 +558,15 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
                 const u32x4 xf = read_tr8<kV>(lds_x + p * XB + 32 * j2 * TX::kBytes + (a_xtr ^ ((vp + e) << 5)));
 #pragma unroll
                 for (int q = 0; q < PY; ++q)
-                  if (p + q < 3) acc[e] = mfma(xf, pf[j2][q], acc[e]);
+                  if (p + q < 3) px[e] = mfma(xf, pf[j2][q], px[e]);
               }
           }
         }
         settle();
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[e][r] = __builtin_fmaf(acc[e][r], before, px[e][r]);
 #pragma unroll
         for (int e = 0; e < VN; ++e) {
           const int vt = vp + e;
@@ -704,8 +704,8 @@ struct ScanPlan {
 
 // Sequences are cut into segments that run side by side when heads and
 // sequences alone do not fill the chip: about kTarget workgroups (three for each
-// of 256 compute units, what fits at once) of equal length; 512 measured 273 us
-// and 1024 267 us where 768 take 220 (16384 tokens, 64 heads).
+// of 256 compute units, what fits at once) of equal length: 16384 tokens of 64
+// heads take 205 us, with 512 217, with 1024 224.
 // A segment costs its chunks one and a half times (the states first), and one
 // step for each segment before it, about 1/7 of a chunk's time: with n chunks,
 // sqrt(n / 11) of them a segment is the shortest that pays, and two chunks are
