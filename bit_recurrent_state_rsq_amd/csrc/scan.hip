@@ -599,6 +599,9 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
       load_c(t0 + kL);
     }
 
+    // (the state after a segment is the next segment's own to work out)
+    if (!STATES && c + 1 == c_end && seg < used - 1) break;
+
     // ---- S <- decay S + B^T (w x)
     const float decay = lds_decay[par];
 #pragma unroll
