@@ -719,15 +719,15 @@ struct ScanPlan {
 };
 
 // Sequences are cut into segments that run side by side when heads and
-// sequences alone do not fill the chip: about kTarget workgroups (three for each
-// of 256 compute units, what fits at once) of equal length: 16384 tokens of 64
-// heads take 205 us, with 512 217, with 1024 224.
+// sequences alone do not fill the chip: about `target` workgroups of equal
+// length, three for each of 256 compute units (16384 tokens of 64 heads of 128 x 64
+// bf16 203 us, with 512 217, with 1024 224), or two where d_k lets no third in
+// (8192 tokens of 64 heads of 256 x 64 bf16 179 us, with 768 201; of 16 heads of
+// 128 x 128 fp32 197, 230).
 // A segment costs its chunks one and a half times (the states first), and one
 // step for each segment before it, about 1/7 of a chunk's time: with n chunks,
 // sqrt(n / 11) of them a segment is the shortest that pays, and two chunks are
 // not worth a second pass.
-constexpr int64_t kTarget = 768;
-
 rsq_status plan_scan(const rsq_ssm* p, ScanPlan& w) {
   w.dkp = p->d_k <= 64 ? 64 : p->d_k <= 128 ? 128 : 256;
   w.vblocks = (int)ceil_div(p->d_v, kV);
@@ -735,7 +735,8 @@ rsq_status plan_scan(const rsq_ssm* p, ScanPlan& w) {
   const int64_t longest = ceil_div(p->max_len, kL);
   int64_t total = ceil_div(p->tokens, kL) + p->seqs;
   if (total > longest * p->seqs) total = longest * p->seqs;
-  int64_t per = ceil_div(total * base, kTarget);
+  const int64_t target = w.dkp > (p->dtype == RSQ_BF16 ? 128 : 64) ? 512 : 768;
+  int64_t per = ceil_div(total * base, target);
   while (per * per * 11 < longest) ++per;
   if (per > longest || longest < 3) per = longest > 0 ? longest : 1;
   w.segs = (int)(longest > 0 ? ceil_div(longest, per) : 1);
