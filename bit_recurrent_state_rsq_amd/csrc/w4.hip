@@ -18,7 +18,8 @@
 // three-input bit operation a pair), and 24 sum(x) is subtracted through a
 // product of x with the constant -24, the accumulator that every weight tile
 // of the group starts from. Products are exact in fp32 (fp32 rows as three
-// bf16 pieces); partial sums reach at most 5.3 times those of the codes alone.
+// bf16 pieces); the offset's sums are gone from the accumulator within a group,
+// from the leading pieces of fp32 rows within 32 columns.
 // int8 rows: int8 products of 16 c (a nibble in the high half of its byte),
 // exact in int32. E4M3 rows are bf16 numbers.
 //
@@ -258,16 +259,25 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
       for (int q = 0; q < GPB; ++q) s[i][q] = b.scale(a, i, q);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      // (fp32 rows are split group by group: their pieces take more registers)
       XFrag<XT> x[4];
+      XRaw<XT> xnow[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) convert_x(xnext[j], x[j]);
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (XT == kXF32) xnow[j] = xnext[j];
+        else convert_x(xnext[j], x[j]);
+      }
       if (m + 1 < MT) load_x(kb, m + 1);
       else if (kb + WAVES < a.kblocks) load_x(kb + WAVES, 0);
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
+        if constexpr (XT == kXF32) {
+#pragma unroll
+          for (int j = 0; j < SPG; ++j) convert_x(xnow[q * SPG + j], x[q * SPG + j]);
+        }
         // scales of this lane's four rows of x in this group
         f32x4 xs = {1.f, 1.f, 1.f, 1.f};
-        if (a.x_groups > 1) {
+        if ((XT == kXInt8 || XT == kXE4m3) && a.x_groups > 1) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int64_t row = m0 + 16 * m + 4 * g + r;
@@ -300,6 +310,38 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) y[i][m][r] = __builtin_fmaf((float)acc[r], sc * xs[r], y[i][m][r]);
           }
+        } else if constexpr (XT == kXF32) {
+          // The leading pieces' products of 32 columns each have a sum of their
+          // own, so that 24 sum(x) is gone again after one rounding at its size: 16
+          // normal rows x 512 x 4736 are off by 8e-8 of the norm (in one sum 8e-7, and
+          // fp32 weights in a library's product 6e-7).
+          constexpr u32x4 minus24 = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
+          const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+          f32x4 start[SPG], rest = zero;
+#pragma unroll
+          for (int j = 0; j < SPG; ++j) {
+            start[j] = mfma(x[q * SPG + j].p[0], minus24, zero);
+#pragma unroll
+            for (int p = XFrag<XT>::kPieces - 1; p > 0; --p) rest = mfma(x[q * SPG + j].p[p], minus24, rest);
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            f32x4 low = rest, acc[SPG];
+#pragma unroll
+            for (int j = 0; j < SPG; ++j) {
+              const u32x4 c = codes_bf16(w[i][q * SPG + j]);
+              acc[j] = mfma(x[q * SPG + j].p[0], c, start[j]);
+#pragma unroll
+              for (int p = XFrag<XT>::kPieces - 1; p > 0; --p) low = mfma(x[q * SPG + j].p[p], c, low);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float v = acc[0][r];
+#pragma unroll
+              for (int j = 1; j < SPG; ++j) v += acc[j][r];
+              y[i][m][r] = __builtin_fmaf(v + low[r], s[i][q] * xs[r], y[i][m][r]);
+            }
+          }
         } else {
           constexpr u32x4 minus24 = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
           f32x4 start = {0.f, 0.f, 0.f, 0.f};
@@ -322,7 +364,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a) {
         }
         // (groups one after another: mixed, they hold registers that cost more in
         // resident wavefronts than their order gains)
-        if constexpr (MT > 1) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MT > 1 || (XT == kXF32 && NT > 2)) __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -366,9 +408,9 @@ struct W4Pick {
 //   above        four, four wavefronts: 33 x 8512 x 2048 9.5, eight 10.9; 16 x 28672 x 8192 31.6, 33.9
 // There 32 rows of x, 64 and more go two times 16 a workgroup: 32 x 28672 x 8192
 // 44, once 16 56; 64 rows 76, 88 (four times 16: 100). Not fp32 rows, whose pieces
-// then leave one wavefront a SIMD (64 rows 177, once 16 146), nor bf16 and E4M3
-// in groups of 32, which keep a start for every group (256 x 4096 x 4096 above
-// 40, once 16 35).
+// then leave one wavefront a SIMD (64 rows 209, once 16 153), nor bf16 and E4M3
+// in groups of 32, which keep a start for every group (256 x 4096 x 4096 39, once
+// 16 31).
 template <int XT, int GROUP>
 W4Pick pick_shape(int M, int tiles) {
   const int64_t mtiles = ceil_div(M, 16), work = tiles * mtiles;
