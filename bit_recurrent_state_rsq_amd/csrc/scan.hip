@@ -7,7 +7,7 @@
 // four small matrix products a chunk, on the matrix cores.
 //
 // Bytes and products would take 61 and 31 us of 16384 tokens (64 heads of 128 x
-// 64, bf16, 283 MB); it takes 203 (1.4 TB/s, 211 TFLOP/s counting the recurrence's
+// 64, bf16, 283 MB); it takes 196 (1.4 TB/s, 219 TFLOP/s counting the recurrence's
 // own 5 operations an element). What that goes to: the state is formed twice (first
 // for the segments' starts, 86 us, then along with y) and from three bf16 pieces
 // each (two would make errors of 2e-6 of an exact fp32 state), so that the matrix
@@ -15,8 +15,8 @@
 // rounding and the diagonal's mask) for 53%, which three wavefronts a SIMD overlap
 // little; registers (168) and LDS (43.5 KB) keep a fourth out. Measured without
 // gain: C B^T made once for all heads of a group, decays of four chunks at a time
-// by four wavefronts (214), raised priority for the products, remainders by dot
-// products.
+// by four wavefronts (5% longer), raised priority for the products, remainders by
+// dot products, more of the segments' states on their way at once.
 // 333 fp32 tokens take 19 us, 9 of them two empty launches.
 #include <initializer_list>
 
@@ -721,7 +721,7 @@ struct ScanPlan {
 // Sequences are cut into segments that run side by side when heads and
 // sequences alone do not fill the chip: about `target` workgroups of equal
 // length, three for each of 256 compute units (16384 tokens of 64 heads of 128 x 64
-// bf16 203 us, with 512 217, with 1024 224), or two where d_k lets no third in
+// bf16 205 us, with 512 217, with 1024 224, measured together), or two where d_k lets no third in
 // (8192 tokens of 64 heads of 256 x 64 bf16 179 us, with 768 201; of 16 heads of
 // 128 x 128 fp32 197, 230).
 // A segment costs its chunks one and a half times (the states first), and one
