@@ -94,7 +94,9 @@ struct Rows {
     const uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
     const uint32_t high = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
     const uint64_t u = (uint64_t)high << 32 | low;
-    const int rows = max(min(len - t0, kL), 0);
+    int rows = min(len - t0, kL);
+    rows = __builtin_amdgcn_readfirstlane(rows);   // (min and max at once would be a vector instruction)
+    rows = max(rows, 0);
     rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0,
                                              __builtin_amdgcn_readfirstlane((int)(rows * row_bytes)), 0x00020000);
   }
@@ -269,10 +271,11 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   const int seg = id % a.segs;
   const int sq = id / a.segs;
   int64_t len64;
-  const int64_t begin = seq_range(a.s.q, sq, len64);
-  const int len = (int)len64;   // rows are counted in 31 bits
+  // (uniform over the workgroup, which the compiler cannot know of loaded offsets)
+  const int64_t begin = __builtin_amdgcn_readfirstlane((int)seq_range(a.s.q, sq, len64));
+  const int len = __builtin_amdgcn_readfirstlane((int)len64);   // rows are counted in 31 bits
   const int dk = a.s.dk, dv = a.s.dv, v0 = vb * kV;
-  const int chunks = (int)((len64 + kL - 1) / kL);
+  const int chunks = (len + kL - 1) / kL;
   const int used = (chunks + a.seg_chunks - 1) / a.seg_chunks;
   // the first pass covers the segments before the last; the second all of them
   if (STATES ? seg >= used - 1 : seg >= used && (seg > 0 || a.s.state_in)) return;
@@ -359,9 +362,9 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     const Rows rC(Cp, crow, t0, end);
 #pragma unroll
     for (int i = 0; i < (STATES ? 0 : KS); ++i) {
-      uint32_t at = coff + (uint32_t)(32 * i * sizeof(T));
-      if (dk < DK) at = 32 * i + 8 * g < dk ? at : kOutside;
-      rc[i].load(rC, at);
+      const uint32_t at = coff + (uint32_t)(32 * i * sizeof(T));
+      if (dk == DK) rc[i].load(rC, at);
+      else rc[i].load(rC, 32 * i + 8 * g < dk ? at : kOutside);
     }
   };
   // a load of fewer than 16 rows (d_k = 256: 8) moves f by the bits of row 8
@@ -600,12 +603,15 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
             for (int r = 0; r < 4; ++r)
               if (tt >= lds_first[par][16 * vt + 4 * g + r]) out[r] = __builtin_nanf("");
           }
-          uint32_t at = yoff + (uint32_t)(16 * vt * sizeof(T));
-          if (v0 + kV > dv) at = v0 + 16 * vt + 4 * g < dv ? at : kOutside;
-          if constexpr (PI == 1)
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(out[0], out[1]), bf16_pair(out[2], out[3])}, rY.rsrc, (int)at, 0, 0);
-          else
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{out[0], out[1], out[2], out[3]}), rY.rsrc, (int)at, 0, 0);
+          const uint32_t at = yoff + (uint32_t)(16 * vt * sizeof(T));
+          auto store = [&](uint32_t at) {
+            if constexpr (PI == 1)
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(out[0], out[1]), bf16_pair(out[2], out[3])}, rY.rsrc, (int)at, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{out[0], out[1], out[2], out[3]}), rY.rsrc, (int)at, 0, 0);
+          };
+          if (v0 + kV <= dv) store(at);
+          else store(v0 + 16 * vt + 4 * g < dv ? at : kOutside);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
