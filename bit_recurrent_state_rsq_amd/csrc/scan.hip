@@ -9,10 +9,10 @@
 // Bytes and products would take 61 and 31 us of 16384 tokens (64 heads of 128 x
 // 64, bf16, 283 MB); it takes 196 (1.4 TB/s, 219 TFLOP/s counting the recurrence's
 // own 5 operations an element). What that goes to: the state is formed twice (first
-// for the segments' starts, 86 us, then along with y) and from three bf16 pieces
+// for the segments' starts, a third of the time, then along with y) and from three bf16 pieces
 // each (two would make errors of 2e-6 of an exact fp32 state), so that the matrix
-// cores are busy for 31% of the cycles and the vector unit (splitting, weighting,
-// rounding and the diagonal's mask) for 53%, which three wavefronts a SIMD overlap
+// cores are busy for 32% of the cycles and the vector unit (splitting, weighting,
+// rounding and the diagonal's mask) for 50%, which three wavefronts a SIMD overlap
 // little; registers (168) and LDS (43.5 KB) keep a fourth out. Measured without
 // gain: C B^T made once for all heads of a group, decays of four chunks at a time
 // by four wavefronts (5% longer), raised priority for the products, remainders by
