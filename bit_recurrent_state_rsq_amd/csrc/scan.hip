@@ -59,14 +59,15 @@ __device__ __forceinline__ uint32_t high_pair(float a, float b) {
 __device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// An fp32 value as N bf16 pieces. One piece is rounded to nearest-even (2^-9
-// relative). Three pieces hold all 24 bits: each takes the leading 8 of what
-// is left, so the products of pieces are exact and their sum is rounded in
-// fp32 only.
+// An fp32 value as N bf16 pieces. Two pieces are each rounded to nearest-even:
+// what they leave out is at most 2^-8 of 2^-8 of the value. Three pieces hold all
+// 24 bits: each takes the leading 8 of what is left, so the products of pieces are
+// exact and their sum is rounded in fp32 only.
 template <int N>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[N]) {
-  if constexpr (N == 1) {
+  if constexpr (N == 2) {
     p[0] = bf16_pair(a, b);
+    p[1] = bf16_pair(a - low_half(p[0]), b - high_half(p[0]));
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -233,12 +234,16 @@ __device__ __forceinline__ void settle() {
 
 // PI pieces of the inputs, PY of the computed factors of y (P and S), 3 of the
 // weighted x that enters the state (a state stays exact to fp32). Products of
-// pieces below 2^-24 are left out.
+// pieces below 2^-24 are left out. bf16 outputs take PY = 2: y before its own
+// rounding is then off by 2^-16 of its terms. (One piece would leave 2^-8 of them,
+// as much as that rounding where the state makes up y; it took 198 us where two take
+// 228, 16384 tokens of 64 heads of 128 x 64.)
 //
-// Shares of the four wavefronts: for y, wavefront w owns the 16 tokens 16 w (so
-// w + 1 tiles of P); for the state, the 16 columns 16 w and all of d_k, in
-// registers over the whole segment. Wavefront 0, with the fewest tiles of P,
-// works out the next chunk's decays. STATES: only the state is wanted (a
+// Shares of the four wavefronts: wavefront w owns the 16 columns 16 w of the state
+// and of y, and all of d_k, in registers over the whole segment; S enters y straight
+// from them. Of P it makes the rows of the 16 tokens 16 w (w + 1 tiles), which pass
+// through LDS, in C's place. Wavefront 0, with the fewest tiles of P, works out the
+// next chunk's decays. STATES: only the state is wanted (a
 // segment before the last, scanned first so that the segments can run side by
 // side).
 template <typename T, int DK, int PI, int PY, bool STATES>
@@ -247,10 +252,12 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   constexpr int KT = DK / 16, KS = DK / 32;
   typedef Tile<DK> TB;
   typedef Tile<kV> TX;
-  constexpr int BB = kL * TB::kBytes, XB = kL * TX::kBytes, SB = kV * TB::kBytes;   // bytes of a piece's tile
+  constexpr int BB = kL * TB::kBytes, XB = kL * TX::kBytes;   // bytes of a piece's tile
   __shared__ __attribute__((aligned(16))) uint8_t lds_b[PI * BB];
   __shared__ __attribute__((aligned(16))) uint8_t lds_x[PI * XB];
-  __shared__ __attribute__((aligned(16))) uint8_t lds_s[STATES ? 16 : PY * SB];   // S^T: [column][key]
+  // C, and once that has been read, P's pieces as products take them: [tokens / 16][s / 32][piece][lane]
+  constexpr int PB = kL / 16 * (kL / 32) * PY * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t lds_c[STATES ? 16 : PI * BB > PB ? PI * BB : PB];
   // of a chunk's tokens, by the chunk's parity: d_t e^{c_L - c_t}, and the factors of e^{c_t - c_s}
   constexpr int LY = STATES ? 4 : kL;
   __shared__ __attribute__((aligned(16))) float lds_w[2][kL], lds_from[2][LY], lds_to[2][LY];
@@ -340,11 +347,10 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   const float Dh = a.s.D ? a.s.D[h] : 0.f;
   const float dt_bias = a.s.dt_bias ? a.s.dt_bias[h] : 0.f;
 
-  // ---- a chunk's rows: B and x go through registers to LDS one chunk ahead,
-  // C's rows 16 wave .. are fragments as they are
+  // ---- a chunk's rows: B, C and x go through registers to LDS one chunk ahead
   constexpr int NB = kL * (DK / 8) / kThreads, RB = kThreads / (DK / 8);   // loads a thread, rows of one load
   constexpr int NX = kL * (kV / 8) / kThreads, RX = kThreads / (kV / 8);
-  Vec8<T, PI> rb[NB], rx[NX], rc[STATES ? 1 : KS];
+  Vec8<T, PI> rb[NB], rx[NX], rc[STATES ? 1 : NB];
   const int bk = (tid % (DK / 8)) * 8, xv8 = (tid % (kV / 8)) * 8;
   uint32_t boff = bk < dk ? (uint32_t)(tid / (DK / 8) * brow + bk * (int)sizeof(T)) : kOutside;
   uint32_t xoff = v0 + xv8 < dv ? (uint32_t)(tid / (kV / 8) * xrow + xv8 * (int)sizeof(T)) : kOutside;
@@ -357,23 +363,19 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
 #pragma unroll
     for (int i = 0; i < NX; ++i) rx[i].load(rX, xoff + (uint32_t)(i * RX * xrow));
   };
-  uint32_t coff = (uint32_t)((16 * wave + n16) * crow + 8 * g * (int)sizeof(T));
+  uint32_t coff = bk < dk ? (uint32_t)(tid / (DK / 8) * crow + bk * (int)sizeof(T)) : kOutside;
   auto load_c = [&](int t0) {
     const Rows rC(Cp, crow, t0, end);
 #pragma unroll
-    for (int i = 0; i < (STATES ? 0 : KS); ++i) {
-      const uint32_t at = coff + (uint32_t)(32 * i * sizeof(T));
-      if (dk == DK) rc[i].load(rC, at);
-      else rc[i].load(rC, 32 * i + 8 * g < dk ? at : kOutside);
-    }
+    for (int i = 0; i < (STATES ? 0 : NB); ++i) rc[i].load(rC, coff + (uint32_t)(i * RB * crow));
   };
   // a load of fewer than 16 rows (d_k = 256: 8) moves f by the bits of row 8
   auto flip = [](int rows) { return (uint32_t)((rows >> 3) & 1 ? 9 << 4 : 0); };
-  uint32_t yoff = (uint32_t)((16 * wave + n16) * yrow + 4 * g * (int)sizeof(T));
+  uint32_t yoff = (uint32_t)(n16 * yrow + (16 * wave + 4 * g) * (int)sizeof(T));
   // LDS addresses of this lane
   uint32_t a_bput = TB::at(tid / (DK / 8), tid % (DK / 8)), a_xput = TX::at(tid / (kV / 8), tid % (kV / 8));
   uint32_t a_frag = TB::fragment(lane), a_btr = TB::transposed(lane), a_xtr = TX::transposed(lane);
-  uint32_t a_sput = TB::four(16 * wave + n16, lane), a_xown = TX::four(16 * wave + n16, lane);
+  uint32_t a_four = TB::four(n16, lane), a_xown = TX::four(n16, lane);
   // Running sums of the log2 decays, in 64 bits: differences of them are small
   // next to the sums where decays are strong. A row past the sequence neither
   // decays nor adds.
@@ -432,8 +434,8 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     const int t0 = c * kL;
     const int par = c & 1;
     local(boff), local(xoff), local(coff), local(yoff), local(a_bput), local(a_xput), local(a_frag), local(a_btr);
-    local(a_xtr), local(a_sput), local(a_xown);
-    // ---- stage: inputs and the state to LDS
+    local(a_xtr), local(a_four), local(a_xown);
+    // ---- stage: inputs to LDS
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       u32x4 p[PI];
@@ -473,13 +475,11 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     }
     if constexpr (!STATES) {
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        uint32_t lo[PY], hi[PY];
-        split_pair<PY>(S[kt][0], S[kt][1], lo);
-        split_pair<PY>(S[kt][2], S[kt][3], hi);
+      for (int i = 0; i < NB; ++i) {
+        u32x4 p[PI];
+        rc[i].pieces(p);
 #pragma unroll
-        for (int q = 0; q < PY; ++q)
-          *reinterpret_cast<u32x2*>(lds_s + q * SB + (a_sput ^ (kt << 5))) = u32x2{lo[q], hi[q]};
+        for (int q = 0; q < PI; ++q) *reinterpret_cast<u32x4*>(lds_c + q * BB + i * RB * TB::kBytes + (a_bput ^ flip(i * RB))) = p[q];
       }
     }
     __syncthreads();
@@ -493,17 +493,50 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     if (tid == kV) lds_bad[par ^ 1] = 0;
 
     if constexpr (!STATES) {
+      // ---- S^T C, 16 tokens a tile: the lane's rows of S, in fours of 32 keys, are the product's
+      f32x4 sc[kL / 16];
+#pragma unroll
+      for (int e = 0; e < kL / 16; ++e) sc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        u32x4 sf[PY];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t lo[PY], hi[PY];
+          split_pair<PY>(S[2 * i + e][0], S[2 * i + e][1], lo);
+          split_pair<PY>(S[2 * i + e][2], S[2 * i + e][3], hi);
+#pragma unroll
+          for (int q = 0; q < PY; ++q) sf[q][2 * e] = lo[q], sf[q][2 * e + 1] = hi[q];
+        }
+#pragma unroll
+        for (int p = 0; p < PI; ++p)
+#pragma unroll
+          for (int e = 0; e < kL / 16; ++e) {
+            const uint8_t* at = lds_c + p * BB + 16 * e * TB::kBytes;
+            const u32x2 c0 = *reinterpret_cast<const u32x2*>(at + (a_four ^ ((2 * i) << 5)));
+            const u32x2 c1 = *reinterpret_cast<const u32x2*>(at + (a_four ^ ((2 * i + 1) << 5)));
+            const u32x4 c = {c0[0], c0[1], c1[0], c1[1]};
+#pragma unroll
+            for (int q = 0; q < PY; ++q)
+              if (p + q < 3) sc[e] = mfma(sf[q], c, sc[e]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      settle();
       u32x4 cf[KS][PI];
 #pragma unroll
-      for (int i = 0; i < KS; ++i) rc[i].pieces(cf[i]);
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int p = 0; p < PI; ++p)
+          cf[i][p] = *reinterpret_cast<const u32x4*>(lds_c + p * BB + 16 * wave * TB::kBytes + (a_frag ^ (i << 6)));
       const int tt = 16 * wave + n16;   // this lane's token
       const int mid = __builtin_amdgcn_readfirstlane(lds_mid[par]);
+      __builtin_amdgcn_sched_barrier(0);
       // y = to_t (2^{n} S^T C + P X), n the middle's power or this token's own
-      const float to = lds_to[par][tt];
       const int power = mid == kWide ? lds_whole[par][tt] : mid;
+      u32x4 pf[kL / 32][PY];
       // ---- P^T (rows s, columns t), two tiles (a k-step of y) at a time, up to
       // the diagonal's; two chains of dependent products run side by side
-      u32x4 pf[kL / 32][PY];
 #pragma unroll
       for (int j2 = 0; j2 < kL / 32; ++j2) {
         if (2 * j2 <= wave) {
@@ -544,139 +577,135 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      // ---- y^T (rows v, columns t), VN tiles of v at a time
-      constexpr int VN = PI == 1 && DK <= 128 ? 2 : 1;
+      auto at_p = [&](int tile, int j2, int q) { return lds_c + (((tile * (kL / 32) + j2) * PY + q) * 64 + lane) * 16; };
+      __syncthreads();   // C has been read
+#pragma unroll
+      for (int j2 = 0; j2 < kL / 32; ++j2)
+        if (2 * j2 <= wave) {
+#pragma unroll
+          for (int q = 0; q < PY; ++q) *reinterpret_cast<u32x4*>(at_p(wave, j2, q)) = pf[j2][q];
+        }
+      __syncthreads();   // P is there
+      // ---- y^T (rows v, columns t), this wavefront's 16 columns
+      u32x4 xf[kL / 32][PI];
+#pragma unroll
+      for (int j2 = 0; j2 < kL / 32; ++j2)
+#pragma unroll
+        for (int p = 0; p < PI; ++p) xf[j2][p] = read_tr8<kV>(lds_x + p * XB + 32 * j2 * TX::kBytes + (a_xtr ^ (wave << 5)));
       const Rows rY(y, yrow, t0, len);
-      const float before = __builtin_amdgcn_ldexpf(1.f, power);
+      __builtin_amdgcn_sched_barrier(0);
+      // y = to_t (2^{n} S^T C + P X), n the middle's power or this token's own
+      float to[kL / 16];
 #pragma unroll
-      for (int vp = 0; vp < kV / 16; vp += VN) {
-        f32x4 acc[VN], px[VN];   // S^T C and P X apart: shorter chains of dependent products
+      for (int e = 0; e < kL / 16; ++e) {
+        to[e] = lds_to[par][16 * e + n16];
+        const float before = __builtin_amdgcn_ldexpf(1.f, mid == kWide ? lds_whole[par][16 * e + n16] : mid);
 #pragma unroll
-        for (int e = 0; e < VN; ++e) acc[e] = px[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < 4; ++r) sc[e][r] *= before;
+      }
 #pragma unroll
-        for (int i = 0; i < KS; ++i)
+      for (int j2 = 0; j2 < kL / 32; ++j2)
 #pragma unroll
-          for (int p = 0; p < PY; ++p)
+        for (int q = 0; q < PY; ++q)
 #pragma unroll
-            for (int e = 0; e < VN; ++e) {
-              const u32x4 sf = *reinterpret_cast<const u32x4*>(lds_s + p * SB + 16 * (vp + e) * TB::kBytes + (a_frag ^ (i << 6)));
-#pragma unroll
-              for (int q = 0; q < PI; ++q)
-                if (p + q < 3) acc[e] = mfma(sf, cf[i][q], acc[e]);
-            }
-#pragma unroll
-        for (int j2 = 0; j2 < kL / 32; ++j2) {
-          if (2 * j2 <= wave) {
+          for (int e = 2 * j2; e < kL / 16; ++e) {
+            const u32x4 pt = *reinterpret_cast<const u32x4*>(at_p(e, j2, q));
 #pragma unroll
             for (int p = 0; p < PI; ++p)
-#pragma unroll
-              for (int e = 0; e < VN; ++e) {
-                const u32x4 xf = read_tr8<kV>(lds_x + p * XB + 32 * j2 * TX::kBytes + (a_xtr ^ ((vp + e) << 5)));
-#pragma unroll
-                for (int q = 0; q < PY; ++q)
-                  if (p + q < 3) px[e] = mfma(xf, pf[j2][q], px[e]);
-              }
+              if (p + q < 3) sc[e] = mfma(xf[j2][p], pt, sc[e]);
           }
+      settle();
+#pragma unroll
+      for (int e = 0; e < kL / 16; ++e) {
+        // D x, from the pieces of x (their sum is exact)
+        float xv[4];
+#pragma unroll
+        for (int p = PI - 1; p >= 0; --p) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(lds_x + p * XB + 16 * e * TX::kBytes + (a_xown ^ (wave << 5)));
+          const float part[4] = {low_half(w[0]), high_half(w[0]), low_half(w[1]), high_half(w[1])};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) xv[r] = p == PI - 1 ? part[r] : xv[r] + part[r];
         }
-        settle();
+        float out[4];
 #pragma unroll
-        for (int e = 0; e < VN; ++e)
+        for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], sc[e][r] * to[e]);
+        if (bad) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[e][r] = __builtin_fmaf(acc[e][r], before, px[e][r]);
-#pragma unroll
-        for (int e = 0; e < VN; ++e) {
-          const int vt = vp + e;
-          // D x, from the pieces of x (their sum is exact)
-          float xv[4];
-#pragma unroll
-          for (int p = PI - 1; p >= 0; --p) {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(lds_x + p * XB + (a_xown ^ (vt << 5)));
-            const float part[4] = {low_half(w[0]), high_half(w[0]), low_half(w[1]), high_half(w[1])};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) xv[r] = p == PI - 1 ? part[r] : xv[r] + part[r];
-          }
-          float out[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], acc[e][r] * to);
-          if (bad) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (tt >= lds_first[par][16 * vt + 4 * g + r]) out[r] = __builtin_nanf("");
-          }
-          const uint32_t at = yoff + (uint32_t)(16 * vt * sizeof(T));
-          auto store = [&](uint32_t at) {
-            if constexpr (PI == 1)
-              __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(out[0], out[1]), bf16_pair(out[2], out[3])}, rY.rsrc, (int)at, 0, 0);
-            else
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{out[0], out[1], out[2], out[3]}), rY.rsrc, (int)at, 0, 0);
-          };
-          if (v0 + kV <= dv) store(at);
-          else store(v0 + 16 * vt + 4 * g < dv ? at : kOutside);
+          for (int r = 0; r < 4; ++r)
+            if (16 * e + n16 >= lds_first[par][16 * wave + 4 * g + r]) out[r] = __builtin_nanf("");
         }
-        __builtin_amdgcn_sched_barrier(0);
+        const uint32_t at = yoff + (uint32_t)(16 * e * yrow);
+        auto store = [&](uint32_t at) {
+          if constexpr (PI == 1)
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(out[0], out[1]), bf16_pair(out[2], out[3])}, rY.rsrc, (int)at, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{out[0], out[1], out[2], out[3]}), rY.rsrc, (int)at, 0, 0);
+        };
+        if (v0 + kV <= dv) store(at);
+        else store(v0 + 16 * wave + 4 * g < dv ? at : kOutside);
       }
       load_c(t0 + kL);
     }
 
     // (the state after a segment is the next segment's own to work out)
-    if (!STATES && c + 1 == c_end && seg < used - 1) break;
-
-    // ---- S <- decay S + B^T (w x)
-    const float decay = lds_decay[par];
+    if (STATES || c + 1 < c_end || seg == used - 1) {
+      // ---- S <- decay S + B^T (w x)
+      const float decay = lds_decay[par];
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[kt][r] *= decay;
-    // Two tiles of keys side by side; the next two are read while they are worked on.
-    constexpr int STEPS = KT / 2 * PI;
-    u32x4 bf[2][2];
-    auto read_b = [&](int ts, int step, u32x4 (&out)[2]) {
-      const int k2 = step / PI * 2, p = step % PI;
+        for (int r = 0; r < 4; ++r) S[kt][r] *= decay;
+      // Two tiles of keys side by side; the next two are read while they are worked on.
+      constexpr int STEPS = KT / 2 * PI;
+      u32x4 bf[2][2];
+      auto read_b = [&](int ts, int step, u32x4 (&out)[2]) {
+        const int k2 = step / PI * 2, p = step % PI;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) out[e] = read_tr8<DK>(lds_b + p * BB + 32 * ts * TB::kBytes + (a_btr ^ ((k2 + e) << 5)));
-    };
-    read_b(0, 0, bf[0]);
+        for (int e = 0; e < 2; ++e) out[e] = read_tr8<DK>(lds_b + p * BB + 32 * ts * TB::kBytes + (a_btr ^ ((k2 + e) << 5)));
+      };
+      read_b(0, 0, bf[0]);
 #pragma unroll
-    for (int ts = 0; ts < kL / 32; ++ts) {
-      u32x4 xr[PI];
+      for (int ts = 0; ts < kL / 32; ++ts) {
+        u32x4 xr[PI];
 #pragma unroll
-      for (int p = 0; p < PI; ++p) xr[p] = read_tr8<kV>(lds_x + p * XB + 32 * ts * TX::kBytes + (a_xtr ^ (wave << 5)));
-      const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds_w[par][32 * ts + 4 * g]);
-      const f32x4 w1 = *reinterpret_cast<const f32x4*>(&lds_w[par][32 * ts + 16 + 4 * g]);
-      u32x4 xw[PW];
+        for (int p = 0; p < PI; ++p) xr[p] = read_tr8<kV>(lds_x + p * XB + 32 * ts * TX::kBytes + (a_xtr ^ (wave << 5)));
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds_w[par][32 * ts + 4 * g]);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&lds_w[par][32 * ts + 16 + 4 * g]);
+        u32x4 xw[PW];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float lo = low_half(xr[PI - 1][i]), hi = high_half(xr[PI - 1][i]);
+        for (int i = 0; i < 4; ++i) {
+          float lo = low_half(xr[PI - 1][i]), hi = high_half(xr[PI - 1][i]);
 #pragma unroll
-        for (int p = PI - 2; p >= 0; --p) lo += low_half(xr[p][i]), hi += high_half(xr[p][i]);
-        lo *= i < 2 ? w0[2 * i] : w1[2 * i - 4];
-        hi *= i < 2 ? w0[2 * i + 1] : w1[2 * i - 3];
-        uint32_t p3[PW];
-        split_pair<PW>(lo, hi, p3);
+          for (int p = PI - 2; p >= 0; --p) lo += low_half(xr[p][i]), hi += high_half(xr[p][i]);
+          lo *= i < 2 ? w0[2 * i] : w1[2 * i - 4];
+          hi *= i < 2 ? w0[2 * i + 1] : w1[2 * i - 3];
+          uint32_t p3[PW];
+          split_pair<PW>(lo, hi, p3);
 #pragma unroll
-        for (int q = 0; q < PW; ++q) xw[q][i] = p3[q];
+          for (int q = 0; q < PW; ++q) xw[q][i] = p3[q];
+        }
+#pragma unroll
+        for (int step = 0; step < STEPS; ++step) {
+          const int now = (ts * STEPS + step) & 1;
+          if (step + 1 < STEPS) read_b(ts, step + 1, bf[now ^ 1]);
+          else if (ts + 1 < kL / 32) read_b(ts + 1, 0, bf[now ^ 1]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int q = 0; q < PW; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (step % PI + q < 3) S[step / PI * 2 + e] = mfma(bf[now][e], xw[q], S[step / PI * 2 + e]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
+      settle();
+      if (bad) {
+        if (lds_first[par][16 * wave + n16] < kL) {
 #pragma unroll
-      for (int step = 0; step < STEPS; ++step) {
-        const int now = (ts * STEPS + step) & 1;
-        if (step + 1 < STEPS) read_b(ts, step + 1, bf[now ^ 1]);
-        else if (ts + 1 < kL / 32) read_b(ts + 1, 0, bf[now ^ 1]);
-        __builtin_amdgcn_sched_barrier(0);
+          for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int q = 0; q < PW; ++q)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (step % PI + q < 3) S[step / PI * 2 + e] = mfma(bf[now][e], xw[q], S[step / PI * 2 + e]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    settle();
-    if (bad) {
-      if (lds_first[par][16 * wave + n16] < kL) {
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[kt][r] = __builtin_nanf("");
+            for (int r = 0; r < 4; ++r) S[kt][r] = __builtin_nanf("");
+        }
       }
     }
     __syncthreads();   // the chunk's LDS has been read
@@ -710,9 +739,9 @@ template <bool STATES>
 ScanFn pick_scan(bool bf16, int dkp) {
   if (bf16) {
     switch (dkp) {
-      case 64: return scan_kernel<Bf16, 64, 1, 1, STATES>;
-      case 128: return scan_kernel<Bf16, 128, 1, 1, STATES>;
-      default: return scan_kernel<Bf16, 256, 1, 1, STATES>;
+      case 64: return scan_kernel<Bf16, 64, 1, 2, STATES>;
+      case 128: return scan_kernel<Bf16, 128, 1, 2, STATES>;
+      default: return scan_kernel<Bf16, 256, 1, 2, STATES>;
     }
   }
   return dkp == 64 ? scan_kernel<float, 64, 3, 3, STATES> : scan_kernel<float, 128, 3, 3, STATES>;
