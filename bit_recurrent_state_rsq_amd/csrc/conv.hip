@@ -342,11 +342,24 @@ extern "C" rsq_status rsq_causal_conv(const rsq_conv* p, void* stream) {
   a.tile = 32;
   while (a.tile > 8 && a.cblocks * ceil_div(p->tokens, a.tile) < 4096) a.tile /= 2;
   a.tiles = (int32_t)ceil_div(p->max_len, (int64_t)a.tile * kWaves);
-  const int64_t blocks = token ? ceil_div(p->seqs * ceil_div(C, v), 256) : (int64_t)a.cblocks * a.tiles * p->seqs;
-  if (blocks > kMaxGrid) return fail(RSQ_E_UNSUPPORTED, "%lld workgroups", (long long)blocks);
   ConvFn fn;
   if (p->dtype == RSQ_BF16) fn = wide ? pick_width<Bf16, 8>(p->width, token, silu) : pick_width<Bf16, 1>(p->width, token, silu);
   else fn = wide ? pick_width<float, 4>(p->width, token, silu) : pick_width<float, 1>(p->width, token, silu);
-  hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * kWaves), 0, (hipStream_t)stream, a);
-  return launched("causal convolution");
+  if (!token) {
+    const int64_t blocks = (int64_t)a.cblocks * a.tiles * p->seqs;
+    if (const rsq_status s = check_blocks(blocks, 64 * kWaves)) return s;
+    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * kWaves), 0, (hipStream_t)stream, a);
+    return launched("causal convolution");
+  }
+  // sequences beyond what one launch may have go into further ones
+  const int64_t cv = ceil_div(C, v), most = max_blocks(256) * 256 / cv;
+  for (int64_t done = 0; done < p->seqs; done += most) {
+    a.q.seqs = (int32_t)(p->seqs - done < most ? p->seqs - done : most);
+    a.x = static_cast<const uint8_t*>(p->x) + done * p->x_stride * size;
+    a.y = static_cast<uint8_t*>(p->y) + done * p->y_stride * size;
+    if (p->state) a.state = static_cast<uint8_t*>(p->state) + done * C * (p->width - 1) * size;
+    hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(a.q.seqs * cv, 256)), dim3(256), 0, (hipStream_t)stream, a);
+    if (const rsq_status s = launched("causal convolution, one token")) return s;
+  }
+  return RSQ_OK;
 }

@@ -54,6 +54,14 @@ inline rsq_status launched(const char* what) {
   return e == hipSuccess ? RSQ_OK : hip_fail(e, what);
 }
 
-constexpr int64_t kMaxGrid = 0x7fffffff;   // blocks along x
+// HIP takes launches of fewer than 2^32 threads along x: the most workgroups of
+// `threads` that one launch may have.
+constexpr int64_t max_blocks(int threads) { return 0xffffffffll / threads; }
+
+// ... refused beyond
+inline rsq_status check_blocks(int64_t blocks, int threads) {
+  if (blocks <= max_blocks(threads)) return RSQ_OK;
+  return fail(RSQ_E_UNSUPPORTED, "%lld workgroups of %d threads: 2^32 threads and more", (long long)blocks, threads);
+}
 
 }  // namespace rsq

@@ -223,7 +223,7 @@ extern "C" rsq_status rsq_rms_norm(const rsq_norm* p, void* stream) {
   const bool codes = p->out_dtype == RSQ_INT8 || p->out_dtype == RSQ_E4M3;
   if (!codes && p->out_dtype != RSQ_F32 && p->out_dtype != RSQ_BF16)
     return fail(RSQ_E_INVALID, "out_dtype %d", p->out_dtype);
-  if (p->rows < 0 || p->rows > kMaxGrid || p->cols < 1)
+  if (p->rows < 0 || p->rows > 0x7fffffff || p->cols < 1)
     return fail(RSQ_E_INVALID, "rows %lld cols %d", (long long)p->rows, p->cols);
   if (p->cols > 32768) return fail(RSQ_E_UNSUPPORTED, "cols %d > 32768", p->cols);
   if (!(p->eps >= 0.f) || p->eps > 3.4e38f) return fail(RSQ_E_INVALID, "eps must be finite and >= 0");
@@ -248,14 +248,24 @@ extern "C" rsq_status rsq_rms_norm(const rsq_norm* p, void* stream) {
   if (const rsq_status s = check_overlap(written, read)) return s;
 
   NormArgs a{};
-  a.x = p->x, a.residual = p->residual, a.weight = p->weight, a.y = p->y, a.scales = p->scales;
+  a.weight = p->weight;
   a.x_stride = p->x_stride, a.r_stride = p->residual_stride, a.y_stride = p->y_stride;
-  a.rows = p->rows, a.cols = p->cols, a.group = p->group, a.eps = p->eps;
+  a.cols = p->cols, a.group = p->group, a.eps = p->eps;
   auto wide = [](const void* q, int64_t stride, int sz, int n) { return aligned(q, n) && stride * sz % n == 0; };
   a.wide = (wide(p->x, p->x_stride, size, 16) ? 1 : 0) |
            (p->residual && wide(p->residual, p->residual_stride, size, 16) ? 2 : 0) |
            (wide(p->y, p->y_stride, osize, codes ? 8 : 16) ? 4 : 0) | (aligned(p->weight, 16) ? 8 : 0);
   const NormPick k = p->dtype == RSQ_BF16 ? pick_out<Bf16>(p->out_dtype, p->cols) : pick_out<float>(p->out_dtype, p->cols);
-  hipLaunchKernelGGL(k.fn, dim3((unsigned)ceil_div(p->rows, k.rows)), dim3(k.threads), 0, (hipStream_t)stream, a);
-  return launched("RMS norm");
+  // rows beyond what one launch may have go into further ones
+  const int64_t most = max_blocks(k.threads) * k.rows, scales = p->group ? p->cols / p->group : 1;
+  for (int64_t done = 0; done < p->rows; done += most) {
+    a.rows = p->rows - done < most ? p->rows - done : most;
+    a.x = static_cast<const uint8_t*>(p->x) + done * p->x_stride * size;
+    if (p->residual) a.residual = static_cast<uint8_t*>(p->residual) + done * p->residual_stride * size;
+    a.y = static_cast<uint8_t*>(p->y) + done * p->y_stride * osize;
+    if (codes) a.scales = p->scales + done * scales;
+    hipLaunchKernelGGL(k.fn, dim3((unsigned)ceil_div(a.rows, k.rows)), dim3(k.threads), 0, (hipStream_t)stream, a);
+    if (const rsq_status s = launched("RMS norm")) return s;
+  }
+  return RSQ_OK;
 }

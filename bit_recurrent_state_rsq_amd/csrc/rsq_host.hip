@@ -723,6 +723,7 @@ rsq_status rsq_decode_ssm_step(rsq_state* st, const rsq_ssm* p, void* stream) {
   }
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
   const rsq::SsmArgs a = rsq::ssm_args(p);
+  if (const rsq_status s = rsq::check_ssm_launches(a)) return s;
   const rsq::SsmGates g{ws + w.q, ws + w.k, ws + w.v, reinterpret_cast<float*>(ws + w.alpha)};
   float* o = reinterpret_cast<float*>(ws + w.o);
   const bool bf16 = p->dtype == RSQ_BF16;

@@ -777,7 +777,7 @@ rsq_status plan_scan(const rsq_ssm* p, ScanPlan& w) {
   w.segs = (int)(longest > 0 ? ceil_div(longest, per) : 1);
   w.seg_chunks = (int)per;
   w.blocks = base * p->seqs * w.segs;
-  if (w.blocks > kMaxGrid) return fail(RSQ_E_UNSUPPORTED, "%lld workgroups", (long long)w.blocks);
+  if (const rsq_status s = check_blocks(w.blocks, kThreads)) return s;
   w.state_bytes = w.bytes = 0;
   if (w.segs > 1) {
     w.state_bytes = (size_t)w.blocks * (w.dkp / 16) * kThreads * 16;

@@ -74,6 +74,8 @@ struct SsmGates {
   void* v;
   float* alpha;
 };
+// Refuses what the two launches below cannot have.
+rsq_status check_ssm_launches(const SsmArgs& a);
 rsq_status launch_ssm_gates(const SsmArgs& a, bool bf16, const SsmGates& out, void* stream);
 // y = o + D x
 rsq_status launch_ssm_skip(const SsmArgs& a, bool bf16, const float* o, void* stream);

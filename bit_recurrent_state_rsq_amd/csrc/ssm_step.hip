@@ -182,6 +182,11 @@ __global__ __launch_bounds__(256) void ssm_skip_kernel(SsmArgs a, const float* o
 
 }  // namespace
 
+rsq_status check_ssm_launches(const SsmArgs& a) {
+  if (const rsq_status s = check_blocks((int64_t)a.q.seqs * a.H, 128)) return s;
+  return check_blocks(ceil_div((int64_t)a.q.seqs * a.H * a.dv, 256), 256);
+}
+
 rsq_status launch_ssm_gates(const SsmArgs& a, bool bf16, const SsmGates& out, void* stream) {
   const unsigned tiles = (unsigned)((int64_t)a.q.seqs * a.H);
   if (bf16) hipLaunchKernelGGL(ssm_gates_kernel<Bf16>, dim3(tiles), dim3(128), 0, (hipStream_t)stream, a, out);
@@ -205,7 +210,7 @@ extern "C" rsq_status rsq_ssm_step(const rsq_ssm* p, void* stream) {
   if (!p->state) return fail(RSQ_E_INVALID, "state is NULL");
   if (const rsq_status s = check_ssm_memory(p)) return s;
   const int64_t blocks = (int64_t)p->seqs * p->heads;
-  if (blocks > kMaxGrid) return fail(RSQ_E_UNSUPPORTED, "%lld workgroups", (long long)blocks);
+  if (const rsq_status s = check_blocks(blocks, 256)) return s;
   const SsmArgs a = ssm_args(p);
   const size_t lds = (size_t)(256 / (p->d_v / 4)) * p->d_v * sizeof(float);   // at most 4 KB
   if (p->dtype == RSQ_BF16)

@@ -120,6 +120,7 @@ __global__ __launch_bounds__(256) void state_load_kernel(StepArgs a, const float
 }  // namespace
 
 rsq_status launch_state_load(const StepArgs& a, int tiles, const float* dense, bool bits32, bool yoked, void* stream) {
+  if (const rsq_status s = check_blocks(tiles, 256)) return s;
   hipLaunchKernelGGL(state_load_kernel, dim3((unsigned)tiles), dim3(256), 0, (hipStream_t)stream, a, dense,
                      bits32 ? 1 : 0, yoked ? 1 : 0);
   return launched("state load");

@@ -480,7 +480,7 @@ extern "C" rsq_status rsq_w4_pack(const int8_t* codes, const void* scales, int32
   PackArgs a{codes, scales, static_cast<uint32_t*>(packed), static_cast<uint8_t*>(packed) + l.codes,
              n, k, group, ssize, l.kblocks, l.npad};
   const int64_t items = (int64_t)l.npad * l.kblocks * (16 + 128 / group);
-  if (ceil_div(items, 256) > kMaxGrid) return fail(RSQ_E_UNSUPPORTED, "weights of %zu bytes", l.total);
+  if (const rsq_status s = check_blocks(ceil_div(items, 256), 256)) return s;
   hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)ceil_div(items, 256)), dim3(256), 0, (hipStream_t)stream, a);
   return launched("4-bit weight packing");
 }

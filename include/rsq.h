@@ -379,12 +379,13 @@ rsq_status rsq_causal_conv(const rsq_conv* conv, void* stream);
  * x, B, C, y and state are 16-byte aligned, the strides of x, B, C and y
  * multiples of 16 bytes; d_k and d_v are multiples of 8.
  * rsq_ssm_scan takes d_k <= 256 (bf16) or 128 (fp32), d_v <= 4096, max_len
- * below 2^31 - 4096 and rows at most 2^24 bytes apart (RSQ_E_UNSUPPORTED beyond). bf16: S and
- * the token weights enter y as two bf16 pieces each (2^-16 of its terms, before y
- * is rounded to bf16); the state itself is exact to fp32. An infinite or NaN x makes its column NaN
- * from its token on; earlier tokens are not touched.
+ * below 2^31 - 4096, rows at most 2^24 bytes apart and seqs * heads *
+ * ceil(d_v / 64) workgroups or more, below 2^24 (RSQ_E_UNSUPPORTED beyond). bf16:
+ * S and the token weights enter y as two bf16 pieces each (2^-16 of its terms,
+ * before y is rounded to bf16); the state itself is exact to fp32. An infinite or
+ * NaN x makes its column NaN from its token on; earlier tokens are not touched.
  * rsq_ssm_step takes one row of every sequence: offsets NULL, max_len 1; d_v <=
- * 1024, d_k <= 4096.
+ * 1024, d_k <= 4096; seqs * heads below 2^24 (RSQ_E_UNSUPPORTED beyond).
  */
 typedef struct rsq_ssm {
   int32_t dtype, seqs, heads, groups, d_k, d_v;

@@ -41,3 +41,41 @@ def test_scan_bf16_factors_keep_sixteen_bits(heads, groups, dk, dv):
     y, got = rsq.ssm_scan(x, dt, A, B, C, dt_bias=bias, softplus=True, state=state, offsets=off, max_len=max(lengths))
     check(y, want, bound, "y")
     check(got, S, bS, "state")
+
+
+# ---------------------------------------------------------------- more rows than one launch has threads for
+
+@pytest.mark.parametrize("out", ["bf16", "int8"])
+def test_norm_rows_of_two_launches(out):
+    """Four rows of 8 columns a workgroup of 256 threads: 2^26 - 4 rows a launch."""
+    edge = (1 << 26) - 4
+    rows = edge + 4099
+    x = torch.zeros(rows, 8, dtype=BF16, device="cuda")
+    res = torch.zeros(rows, 8, dtype=BF16, device="cuda")
+    r = gen(3)
+    w = r(8)
+    some = torch.cat([torch.arange(0, 70), torch.arange(edge - 70, edge + 70), torch.arange(rows - 70, rows)]).cuda()
+    x[some], res[some] = r(len(some), 8, dtype=BF16), r(len(some), 8, dtype=BF16)
+    few = res[some]
+    want = rsq.rms_norm(x[some], w, residual=few, out_dtype=out)
+    got = rsq.rms_norm(x, w, residual=res, out_dtype=out)
+    assert torch.equal(res[some], few)
+    for a, b in zip(got if out == "int8" else [got], want if out == "int8" else [want]):
+        assert torch.equal(a[some], b)
+
+
+def test_conv_tokens_of_two_launches():
+    """An element a lane (an odd number of channels): 2^32 - 256 of them a launch."""
+    C = 4353
+    per = ((1 << 32) - 256) // C
+    n = per + 2000
+    x = torch.zeros(n, C, dtype=BF16, device="cuda")
+    st = torch.zeros(n, C, 1, dtype=BF16, device="cuda")
+    r = gen(4)
+    w, b = r(C, 2), r(C)
+    some = torch.cat([torch.arange(0, 5), torch.arange(per - 5, per + 5), torch.arange(n - 5, n)]).cuda()
+    x[some], st[some] = r(len(some), C, dtype=BF16), r(len(some), C, 1, dtype=BF16)
+    few = st[some]
+    want = rsq.causal_conv_step(x[some], w, b, state=few, activation="silu")
+    y = rsq.causal_conv_step(x, w, b, state=st, activation="silu")
+    assert torch.equal(y[some], want) and torch.equal(st[some], few)

@@ -1,0 +1,36 @@
+"""Sizes of the layer operators at the edge of what one launch may have (2^32 threads along x). No GPU is used:
+every call here is a query, or is refused before the library touches a device."""
+import ctypes
+
+import pytest
+
+rsq = pytest.importorskip("bit_recurrent_state_rsq_amd")
+from bit_recurrent_state_rsq_amd import _abi  # noqa: E402
+from bit_recurrent_state_rsq_amd._abi import lib  # noqa: E402
+from test_layer_refusals import SSM, UNSUPPORTED, fill  # noqa: E402
+
+
+def ssm(seqs, heads, max_len=1, d_v=8, **kw):
+    """Equal sequences of 8 x d_v states in memory wide enough for all of them."""
+    far = 1 << 40
+    return fill(_abi.Ssm, {**SSM, "seqs": seqs, "heads": heads, "groups": 1, "d_k": 8, "d_v": d_v,
+                           "tokens": seqs * max_len, "max_len": max_len, "x": far, "x_stride": heads * d_v, "B": 2 * far,
+                           "b_stride": 8, "C": 3 * far, "c_stride": 8, "dt": 4 * far, "dt_stride": heads, "state": 5 * far,
+                           "y": 6 * far, "y_stride": heads * d_v, "D": None, "dt_bias": None, "A": 7 * far, **kw})
+
+
+@pytest.mark.parametrize("seqs,heads,d_v,fits", [((1 << 24) - 1, 1, 8, True), (1 << 24, 1, 8, False), (1 << 20, 16, 64, False),
+                                                (1 << 20, 8, 72, False), ((1 << 20) - 1, 8, 128, True)])
+def test_scan_workgroups(seqs, heads, d_v, fits):
+    """256 threads a workgroup, one per sequence, head and 64 columns."""
+    p, n = ssm(seqs, heads, d_v=d_v), ctypes.c_size_t()
+    code = lib.rsq_ssm_scan_workspace(ctypes.byref(p), ctypes.byref(n))
+    assert code == (0 if fits else UNSUPPORTED)
+    if not fits:
+        assert lib.rsq_ssm_scan(ctypes.byref(p), None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("seqs,heads", [(1 << 24, 1), (1 << 18, 64)])
+def test_step_workgroups(seqs, heads):
+    p = ssm(seqs, heads)
+    assert lib.rsq_ssm_step(ctypes.byref(p), None) == UNSUPPORTED
