@@ -40,11 +40,12 @@ constexpr int kWide = 1 << 30;   // no power of two
 
 struct ScanArgs {
   SsmArgs s;
-  float* ws_state;    // [seqs][heads][column blocks][segments][DK / 16][256] float4
-  float* ws_decay;    // [seqs][heads][segments]: log2 of a segment's decay
+  float* ws_state;    // [heads][column blocks][slots][DK / 16][256] float4
+  float* ws_decay;    // [heads][slots]: log2 of a segment's decay
   int32_t vblocks;    // column blocks of kV
   int32_t segs;       // segments of the longest sequence
   int32_t seg_chunks; // chunks of a segment
+  int32_t slots;      // segments of all sequences that are cut into two and more
 };
 
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -232,6 +233,75 @@ __device__ __forceinline__ void settle() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// What a workgroup scans: a segment of a sequence that is cut into `used` of them,
+// or a whole one (used 1).
+struct Share {
+  int seq, seg, used;
+  int slot;         // of the sequence's first segment
+  int begin, len;   // the sequence's rows (counted in 31 bits)
+};
+
+__device__ __forceinline__ void read_sequence(const ScanArgs& a, int s, int& begin, int& len) {
+  int64_t n;
+  begin = (int)seq_range(a.s.q, s, n);
+  len = (int)n;
+}
+
+// segments of a sequence, none if it is not cut
+__device__ __forceinline__ int cut_segments(const ScanArgs& a, int len) {
+  const int chunks = (len + kL - 1) / kL;
+  const int used = (chunks + a.seg_chunks - 1) / a.seg_chunks;
+  return used > 1 ? used : 0;
+}
+
+// Units of work: the segments of the sequences that are cut, in the sequences'
+// order (a unit's number is its slot in the workspace), then every sequence once,
+// for those that are not. Where the offsets fall, sequences overlap and may have
+// more segments than the workspace has slots: the ones that do not fit are scanned
+// whole. False for a unit without work. The wavefronts all find the same, each
+// for itself: 64 sequences at a time, with the sequences before to be counted
+// only where a sequence is cut.
+__device__ __forceinline__ bool find_share(const ScanArgs& a, int unit, int lane, Share& f) {
+  if (!a.s.q.offsets) {
+    f.used = a.segs;
+    f.seq = unit / a.segs;
+    f.slot = f.seq * a.segs;
+    f.seg = unit - f.slot;
+    read_sequence(a, f.seq, f.begin, f.len);
+    return true;
+  }
+  const bool whole = unit >= a.slots;
+  const int own = unit - a.slots, seqs = a.s.q.seqs;
+  f = Share{own, 0, 1, 0, 0, 0};
+  if (whole) {
+    read_sequence(a, own, f.begin, f.len);
+    f.begin = __builtin_amdgcn_readfirstlane(f.begin), f.len = __builtin_amdgcn_readfirstlane(f.len);
+    if (cut_segments(a, f.len) == 0) return true;
+  }
+  int first = 0;   // slots of the sequences before these 64
+  for (int s0 = 0; s0 < seqs && first <= a.slots; s0 += 64) {
+    const int s = s0 + lane;
+    int begin = 0, len = 0;
+    if (s < seqs) read_sequence(a, s, begin, len);
+    const int n = cut_segments(a, len);
+    const int upto = (int)wave_scan((double)n);
+    const uint64_t hit = __builtin_amdgcn_ballot_w64(whole ? s == own : unit < first + upto);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      const int end = first + __builtin_amdgcn_readlane(upto, l);
+      if (whole) return end > a.slots;
+      f.used = __builtin_amdgcn_readlane(n, l);
+      f.seq = s0 + l;
+      f.slot = end - f.used;
+      f.seg = unit - f.slot;
+      f.begin = __builtin_amdgcn_readlane(begin, l), f.len = __builtin_amdgcn_readlane(len, l);
+      return end <= a.slots;
+    }
+    first += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return whole;
+}
+
 // PI pieces of the inputs, PY of the computed factors of y (P and S), 3 of the
 // weighted x that enters the state (a state stays exact to fp32). Products of
 // pieces below 2^-24 are left out. bf16 outputs take PY = 2: y before its own
@@ -275,25 +345,28 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   id /= a.s.H;
   const int vb = id % a.vblocks;
   id /= a.vblocks;
-  const int seg = id % a.segs;
-  const int sq = id / a.segs;
-  int64_t len64;
-  // (uniform over the workgroup, which the compiler cannot know of loaded offsets)
-  const int64_t begin = __builtin_amdgcn_readfirstlane((int)seq_range(a.s.q, sq, len64));
-  const int len = __builtin_amdgcn_readfirstlane((int)len64);   // rows are counted in 31 bits
+  const float A2 = a.s.A[h] * 1.44269504088896f;   // decays in powers of two
+  const float Dh = a.s.D ? a.s.D[h] : 0.f;
+  const float dt_bias = a.s.dt_bias ? a.s.dt_bias[h] : 0.f;
+  Share share;
+  if (!find_share(a, id, lane, share)) return;
+  // (all uniform over the workgroup, which the compiler cannot know of loaded offsets)
+  const int sq = __builtin_amdgcn_readfirstlane(share.seq), seg = __builtin_amdgcn_readfirstlane(share.seg);
+  const int used = __builtin_amdgcn_readfirstlane(share.used), slot0 = __builtin_amdgcn_readfirstlane(share.slot);
+  const int64_t begin = __builtin_amdgcn_readfirstlane(share.begin);
+  const int len = __builtin_amdgcn_readfirstlane(share.len);
   const int dk = a.s.dk, dv = a.s.dv, v0 = vb * kV;
   const int chunks = (len + kL - 1) / kL;
-  const int used = (chunks + a.seg_chunks - 1) / a.seg_chunks;
   // the first pass covers the segments before the last; the second all of them
-  if (STATES ? seg >= used - 1 : seg >= used && (seg > 0 || a.s.state_in)) return;
+  if (STATES ? seg == used - 1 : chunks == 0 && a.s.state_in) return;
 
   // ---- the state before the segment
   f32x4 S[KT];   // S[kt][r] = state[16 kt + 4 g + r][v0 + 16 wave + n16]
   const int sv = v0 + 16 * wave + n16;
   float* st = a.s.state + ((size_t)sq * a.s.H + h) * dk * dv + sv;
   const size_t slot = (size_t)KT * kThreads;
-  f32x4* ws = reinterpret_cast<f32x4*>(a.ws_state) + (((size_t)sq * a.s.H + h) * a.vblocks + vb) * a.segs * slot + tid;
-  float* wd = a.ws_decay + ((size_t)sq * a.s.H + h) * a.segs;
+  f32x4* ws = reinterpret_cast<f32x4*>(a.ws_state) + (((size_t)h * a.vblocks + vb) * a.slots + slot0) * slot + tid;
+  float* wd = a.ws_decay + (size_t)h * a.slots + slot0;
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
   const bool split = used > 1;
@@ -311,10 +384,10 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
     // the last segment's slot, which no segment's own state takes
     if (seg == 0)
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) ws[(size_t)(a.segs - 1) * slot + kt * kThreads] = S[kt];
+      for (int kt = 0; kt < KT; ++kt) ws[(size_t)(used - 1) * slot + kt * kThreads] = S[kt];
   } else if (split) {
     // slot 0 holds the state after segment 0, slot j > 0 what segment j adds
-    const size_t first = seg == 0 ? a.segs - 1 : 0;
+    const size_t first = seg == 0 ? used - 1 : 0;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) S[kt] = ws[first * slot + kt * kThreads];
     // (the next segment's state is on its way while one is added)
@@ -343,9 +416,6 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   T* y = reinterpret_cast<T*>(a.s.y) + begin * a.s.y_stride + (size_t)h * dv + v0;
   const int xrow = (int)(a.s.x_stride * sizeof(T)), brow = (int)(a.s.b_stride * sizeof(T));
   const int crow = (int)(a.s.c_stride * sizeof(T)), yrow = (int)(a.s.y_stride * sizeof(T));
-  const float A2 = a.s.A[h] * 1.44269504088896f;   // decays in powers of two
-  const float Dh = a.s.D ? a.s.D[h] : 0.f;
-  const float dt_bias = a.s.dt_bias ? a.s.dt_bias[h] : 0.f;
 
   // ---- a chunk's rows: B, C and x go through registers to LDS one chunk ahead
   constexpr int NB = kL * (DK / 8) / kThreads, RB = kThreads / (DK / 8);   // loads a thread, rows of one load
@@ -354,7 +424,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   const int bk = (tid % (DK / 8)) * 8, xv8 = (tid % (kV / 8)) * 8;
   uint32_t boff = bk < dk ? (uint32_t)(tid / (DK / 8) * brow + bk * (int)sizeof(T)) : kOutside;
   uint32_t xoff = v0 + xv8 < dv ? (uint32_t)(tid / (kV / 8) * xrow + xv8 * (int)sizeof(T)) : kOutside;
-  const int c_end = min(chunks, (seg + 1) * a.seg_chunks);
+  const int c_end = split ? min(chunks, (seg + 1) * a.seg_chunks) : chunks;
   const int end = min(len, c_end * kL);   // (int: c_end * kL is below len + kL)
   auto load_bx = [&](int t0) {
     const Rows rB(Bp, brow, t0, end), rX(x, xrow, t0, end);
@@ -716,7 +786,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) ws[(size_t)seg * slot + kt * kThreads] = S[kt];
     if (tid == 0 && vb == 0) wd[seg] = (float)total;
-  } else if (seg == (used > 0 ? used - 1 : 0)) {
+  } else if (seg == used - 1) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -748,8 +818,8 @@ ScanFn pick_scan(bool bf16, int dkp) {
 }
 
 struct ScanPlan {
-  int dkp, vblocks, segs, seg_chunks;
-  int64_t blocks;
+  int dkp, vblocks, segs, seg_chunks, slots;
+  int64_t state_blocks, blocks;   // of the first and of the second pass
   size_t state_bytes, bytes;
 };
 
@@ -763,6 +833,13 @@ struct ScanPlan {
 // step for each segment before it, about 1/7 of a chunk's time: with n chunks,
 // sqrt(n / 11) of them a segment is the shortest that pays, and two chunks are
 // not worth a second pass.
+//
+// Of packed sequences only the longest is known here. With their rows apart, a
+// sequence of len rows has at most (len - 1) / (64 per) segments after its first, so
+// all have at most tokens / (64 per), and the sequences that are cut are at most as
+// many: one prompt of 16384 tokens beside 255 of one (64 heads of 128 x 64 bf16)
+// needs 25 MB and 16768 workgroups, where a slot for each sequence's longest would
+// take 3.2 GB and 98304.
 rsq_status plan_scan(const rsq_ssm* p, ScanPlan& w) {
   w.dkp = p->d_k <= 64 ? 64 : p->d_k <= 128 ? 128 : 256;
   w.vblocks = (int)ceil_div(p->d_v, kV);
@@ -776,13 +853,18 @@ rsq_status plan_scan(const rsq_ssm* p, ScanPlan& w) {
   if (per > longest || longest < 3) per = longest > 0 ? longest : 1;
   w.segs = (int)(longest > 0 ? ceil_div(longest, per) : 1);
   w.seg_chunks = (int)per;
-  w.blocks = base * p->seqs * w.segs;
-  if (const rsq_status s = check_blocks(w.blocks, kThreads)) return s;
-  w.state_bytes = w.bytes = 0;
-  if (w.segs > 1) {
-    w.state_bytes = (size_t)w.blocks * (w.dkp / 16) * kThreads * 16;
-    w.bytes = w.state_bytes + (size_t)p->seqs * p->heads * w.segs * 4;
+  int64_t slots = w.segs > 1 ? (int64_t)p->seqs * w.segs : 0;
+  if (p->offsets) {
+    const int64_t more = p->tokens / (kL * per);
+    const int64_t most = more + (more < p->seqs ? more : p->seqs);
+    if (slots > most) slots = most;
   }
+  w.state_blocks = base * slots;
+  w.blocks = base * (p->offsets || w.segs == 1 ? slots + p->seqs : slots);
+  if (const rsq_status s = check_blocks(w.blocks, kThreads)) return s;
+  w.slots = (int)slots;
+  w.state_bytes = (size_t)w.state_blocks * (w.dkp / 16) * kThreads * 16;
+  w.bytes = w.state_bytes + (size_t)p->heads * slots * 4;
   return RSQ_OK;
 }
 
@@ -821,10 +903,10 @@ extern "C" rsq_status rsq_ssm_scan(const rsq_ssm* p, void* stream) {
   a.s = ssm_args(p);
   a.ws_state = static_cast<float*>(p->workspace);
   a.ws_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(p->workspace) + w.state_bytes);
-  a.vblocks = w.vblocks, a.segs = w.segs, a.seg_chunks = w.seg_chunks;
+  a.vblocks = w.vblocks, a.segs = w.segs, a.seg_chunks = w.seg_chunks, a.slots = w.slots;
   const bool bf16 = p->dtype == RSQ_BF16;
-  if (w.segs > 1) {
-    hipLaunchKernelGGL(pick_scan<true>(bf16, w.dkp), dim3((unsigned)w.blocks), dim3(kThreads), 0, (hipStream_t)stream, a);
+  if (w.slots > 0) {
+    hipLaunchKernelGGL(pick_scan<true>(bf16, w.dkp), dim3((unsigned)w.state_blocks), dim3(kThreads), 0, (hipStream_t)stream, a);
     if (const rsq_status s = launched("selective scan, segment states")) return s;
   }
   hipLaunchKernelGGL(pick_scan<false>(bf16, w.dkp), dim3((unsigned)w.blocks), dim3(kThreads), 0, (hipStream_t)stream, a);

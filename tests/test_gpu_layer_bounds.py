@@ -79,3 +79,45 @@ def test_conv_tokens_of_two_launches():
     want = rsq.causal_conv_step(x[some], w, b, state=few, activation="silu")
     y = rsq.causal_conv_step(x, w, b, state=st, activation="silu")
     assert torch.equal(y[some], want) and torch.equal(st[some], few)
+
+
+# ---------------------------------------------------------------- ragged batches
+
+def scan_bounded(case, off, seqs, state, longest):
+    """ssm_scan within the reference's bounds, rows of no sequence untouched."""
+    x, dt, A, B, C, D, bias = case
+    want, S, by, bS = ref.scan(x, dt, A, B, C, D, bias, True, state, seqs, x.dtype)
+    out = torch.full(x.shape, 7.0, dtype=x.dtype, device="cuda")
+    y, got = rsq.ssm_scan(x, dt, A, B, C, D=D, dt_bias=bias, softplus=True, state=state, offsets=off, max_len=longest, out=out)
+    inside = torch.zeros(x.shape[0], dtype=torch.bool)
+    for a, m in seqs:
+        inside[a: a + m] = True
+    check(y[inside.cuda()], want[inside], by[inside], "y")
+    check(got, S, bS, "state")
+    assert (y[~inside.cuda()] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("given", [True, False])
+def test_scan_long_prompts_among_hundreds(dtype, given):
+    """Cut prompts at the front, in the middle and at the end of 200 sequences of a few tokens or none."""
+    lengths = [n % 4 for n in range(200)]
+    lengths[1], lengths[70], lengths[130], lengths[199] = 900, 400, 321, 700
+    case = ssm_case(sum(lengths) + 5, 2, 1, 16, 16, dtype, seed=2)
+    off, _ = offsets_of(lengths, 2, 3)
+    seqs = [(int(a), n) for a, n in zip(off[:-1].tolist(), lengths)]
+    scan_bounded(case, off, seqs, gen(5)(200, 2, 16, 16) if given else None, 900)
+
+
+def test_scan_falling_offsets_of_long_sequences():
+    """Sequences over the same rows have more segments than rows allow for: those that do not fit run whole."""
+    n = 700
+    case = ssm_case(n, 2, 1, 16, 16, F32, seed=3)
+    off = torch.tensor([0, n] * 6 + [300, n], dtype=torch.int32).cuda()
+    o = off.tolist()
+    seqs = [(a, max(0, b - a)) for a, b in zip(o[:-1], o[1:])]
+    x, dt, A, B, C, D, bias = case
+    want, S, by, bS = ref.scan(x, dt, A, B, C, D, bias, True, None, seqs, F32)
+    y, got = rsq.ssm_scan(x, dt, A, B, C, D=D, dt_bias=bias, softplus=True, offsets=off, max_len=n)
+    check(got, S, bS, "state")
+    assert torch.isfinite(y).all()

@@ -7,7 +7,7 @@ import pytest
 rsq = pytest.importorskip("bit_recurrent_state_rsq_amd")
 from bit_recurrent_state_rsq_amd import _abi  # noqa: E402
 from bit_recurrent_state_rsq_amd._abi import lib  # noqa: E402
-from test_layer_refusals import SSM, UNSUPPORTED, fill  # noqa: E402
+from test_layer_refusals import SSM, UNSUPPORTED, addr, fill  # noqa: E402
 
 
 def ssm(seqs, heads, max_len=1, d_v=8, **kw):
@@ -34,3 +34,15 @@ def test_scan_workgroups(seqs, heads, d_v, fits):
 def test_step_workgroups(seqs, heads):
     p = ssm(seqs, heads)
     assert lib.rsq_ssm_step(ctypes.byref(p), None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("seqs,tokens,max_len", [(256, 16384 + 255, 16384), (1024, 65536, 60000), (2000, 1 << 20, 1 << 19)])
+def test_scan_workspace_goes_by_the_segments_that_exist(seqs, tokens, max_len):
+    """One long prompt beside many short ones: the slots of at most every 64 per rows and of as many sequences, at the
+    head's 128 x 64 fp32 state and its decay each. More than three segments for each of 768 workgroups are never wanted."""
+    p = fill(_abi.Ssm, {**SSM, "seqs": seqs, "heads": 64, "groups": 1, "tokens": tokens, "max_len": max_len,
+                        "offsets": addr(9), "x_stride": 4096, "b_stride": 128, "c_stride": 128, "dt_stride": 64,
+                        "y_stride": 4096})
+    n = ctypes.c_size_t()
+    assert lib.rsq_ssm_scan_workspace(ctypes.byref(p), ctypes.byref(n)) == 0
+    assert 0 < n.value <= 3 * 768 * (128 * 64 * 4 + 4)
