@@ -33,6 +33,7 @@ struct ConvArgs {
   int32_t C;
   int32_t cblocks, tiles;   // blocks along the channels; blocks along a sequence
   int32_t tile;             // tokens of a wavefront
+  int32_t per, last;        // listed blocks: how many a workgroup takes, and the last workgroup along them
 };
 
 // exp(-v) saturates to infinity for v below about -88, where silu(v) rounds to
@@ -144,18 +145,9 @@ __device__ __forceinline__ void store_state(T* p, const float (&h)[W - 1][VEC]) 
   }
 }
 
+// One wavefront's tile of a sequence: channels c .. of tokens t0 ..
 template <typename T, int W, int VEC, bool SILU>
-__global__ __launch_bounds__(64 * kWaves) void conv_prompt_kernel(ConvArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t id = blockIdx.x;
-  const int cb = (int)(id % a.cblocks);
-  id /= a.cblocks;
-  const int64_t tile = id % a.tiles;
-  const int s = (int)(id / a.tiles);
-  int64_t len;
-  const int64_t begin = seq_range(a.q, s, len);
-  const int64_t t0 = (tile * kWaves + wave) * a.tile;
-  const int c = (cb * 64 + lane) * VEC;
+__device__ __forceinline__ void conv_tile(const ConvArgs& a, int s, int64_t begin, int64_t len, int64_t t0, int c) {
   if (c >= a.C || t0 >= len) return;   // (an empty sequence keeps its state)
   const T* x = reinterpret_cast<const T*>(a.x) + begin * a.x_stride + c;
   T* y = reinterpret_cast<T*>(a.y) + begin * a.y_stride + c;
@@ -234,6 +226,67 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompt_kernel(ConvArgs a) {
   }
 }
 
+// A workgroup for every block of tokens (kWaves tiles) and of channels that the
+// longest sequence has, in every sequence.
+template <typename T, int W, int VEC, bool SILU>
+__global__ __launch_bounds__(64 * kWaves) void conv_prompt_kernel(ConvArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t id = blockIdx.x;
+  const int cb = (int)(id % a.cblocks);
+  id /= a.cblocks;
+  const int64_t tile = id % a.tiles;
+  const int s = (int)(id / a.tiles);
+  int64_t len;
+  const int64_t begin = seq_range(a.q, s, len);
+  conv_tile<T, W, VEC, SILU>(a, s, begin, len, (tile * kWaves + wave) * a.tile, (cb * 64 + lane) * VEC);
+}
+
+// sum over the lanes up to this one
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Only the blocks that sequences have, listed sequence by sequence: `per` of them
+// in a row for a workgroup, all that are left for the last one (where offsets fall
+// there may be more than rows allow for). Wavefronts search the offsets for their first block, and
+// for the next sequence with tokens, 64 sequences at a time.
+template <typename T, int W, int VEC, bool SILU>
+__global__ __launch_bounds__(64 * kWaves) void conv_list_kernel(ConvArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int cb = (int)(blockIdx.x % a.cblocks), group = (int)(blockIdx.x / a.cblocks);
+  const int rows = a.tile * kWaves;
+  int64_t left = group == a.last ? INT64_MAX : a.per;
+  int64_t skip = (int64_t)group * a.per;   // blocks before the wanted one, in sequences s0 and on
+  int64_t s0 = 0;
+  if (!a.q.offsets) s0 = skip / a.tiles, skip -= s0 * a.tiles;
+  while (s0 < a.q.seqs) {
+    int64_t begin = 0, len = 0;
+    if (s0 + lane < a.q.seqs) begin = seq_range(a.q, (int)(s0 + lane), len);
+    const int n = (int)((len + rows - 1) / rows);
+    const int upto = wave_scan(n, lane);
+    const uint64_t hit = __builtin_amdgcn_ballot_w64(skip < upto);
+    if (!hit) {
+      skip -= __builtin_amdgcn_readlane(upto, 63);
+      s0 += 64;
+      continue;
+    }
+    const int l = __builtin_ctzll(hit);
+    const int mine = __builtin_amdgcn_readlane(n, l);
+    const int64_t first = __builtin_amdgcn_readlane((int)begin, l), tokens = __builtin_amdgcn_readlane((int)len, l);
+    for (int tile = (int)(skip - (__builtin_amdgcn_readlane(upto, l) - mine)); tile < mine; ++tile) {
+      conv_tile<T, W, VEC, SILU>(a, (int)(s0 + l), first, tokens, ((int64_t)tile * kWaves + wave) * a.tile, (cb * 64 + lane) * VEC);
+      if (--left == 0) return;
+    }
+    s0 += l + 1;
+    skip = 0;
+  }
+}
+
 // One token of every sequence: a lane per VEC channels of a sequence. The state
 // (W - 1 inputs a channel, read and written) is most of the traffic. 128
 // sequences of 4352 channels (9 MB) take 5.3 us, where an empty launch takes 4.6.
@@ -271,18 +324,21 @@ __global__ __launch_bounds__(256) void conv_token_kernel(ConvArgs a) {
 
 typedef void (*ConvFn)(ConvArgs);
 
+enum ConvForm { kToken, kBlocks, kList };
+
 template <typename T, int W, int VEC>
-ConvFn pick(bool token, bool silu) {
-  if (token) return silu ? conv_token_kernel<T, W, VEC, true> : conv_token_kernel<T, W, VEC, false>;
+ConvFn pick(ConvForm form, bool silu) {
+  if (form == kToken) return silu ? conv_token_kernel<T, W, VEC, true> : conv_token_kernel<T, W, VEC, false>;
+  if (form == kList) return silu ? conv_list_kernel<T, W, VEC, true> : conv_list_kernel<T, W, VEC, false>;
   return silu ? conv_prompt_kernel<T, W, VEC, true> : conv_prompt_kernel<T, W, VEC, false>;
 }
 
 template <typename T, int VEC>
-ConvFn pick_width(int width, bool token, bool silu) {
+ConvFn pick_width(int width, ConvForm form, bool silu) {
   switch (width) {
-    case 2: return pick<T, 2, VEC>(token, silu);
-    case 3: return pick<T, 3, VEC>(token, silu);
-    default: return pick<T, 4, VEC>(token, silu);
+    case 2: return pick<T, 2, VEC>(form, silu);
+    case 3: return pick<T, 3, VEC>(form, silu);
+    default: return pick<T, 4, VEC>(form, silu);
   }
 }
 
@@ -342,12 +398,30 @@ extern "C" rsq_status rsq_causal_conv(const rsq_conv* p, void* stream) {
   a.tile = 32;
   while (a.tile > 8 && a.cblocks * ceil_div(p->tokens, a.tile) < 4096) a.tile /= 2;
   a.tiles = (int32_t)ceil_div(p->max_len, (int64_t)a.tile * kWaves);
+  const int64_t blocks = (int64_t)a.cblocks * a.tiles * p->seqs;
+  // Of packed sequences with their rows apart, at most `listed` blocks have tokens.
+  // A workgroup without any costs 0.8 ns, finding the others' blocks about 1 ns each
+  // for every 64 sequences that are searched. us with blocks of all sequences and
+  // with listed ones, 16384 x 4352 bf16: 8 sequences, 2.8 times the listed blocks 67
+  // and 69, 4.2 times 62 and 59; 16345 tokens among 39 of one 82 and 59; 16384 beside
+  // 255 of one 276 and 70. 65536 tokens with one of 60000 among 1024 sequences 3430
+  // and 339; 1024 equal ones of 64 (1024 channels) 58 and 101.
+  const int64_t rows = (int64_t)a.tile * kWaves, listed = p->offsets ? p->tokens / rows + p->seqs : (int64_t)a.tiles * p->seqs;
+  const bool list = !token && (blocks > max_blocks(64 * kWaves) || blocks > 4 * listed * a.cblocks);
+  const ConvForm form = token ? kToken : list ? kList : kBlocks;
   ConvFn fn;
-  if (p->dtype == RSQ_BF16) fn = wide ? pick_width<Bf16, 8>(p->width, token, silu) : pick_width<Bf16, 1>(p->width, token, silu);
-  else fn = wide ? pick_width<float, 4>(p->width, token, silu) : pick_width<float, 1>(p->width, token, silu);
+  if (p->dtype == RSQ_BF16) fn = wide ? pick_width<Bf16, 8>(p->width, form, silu) : pick_width<Bf16, 1>(p->width, form, silu);
+  else fn = wide ? pick_width<float, 4>(p->width, form, silu) : pick_width<float, 1>(p->width, form, silu);
+  if (list) {
+    // (more in a row where each search is long; one of 20000 tokens among 20000 short ones 2152 us, one by one 35000)
+    a.per = (int32_t)(1 + p->seqs / 256 + listed * a.cblocks / max_blocks(64 * kWaves));
+    const int64_t groups = ceil_div(listed, a.per);
+    a.last = (int32_t)(groups - 1);
+    if (const rsq_status s = check_blocks(groups * a.cblocks, 64 * kWaves)) return s;
+    hipLaunchKernelGGL(fn, dim3((unsigned)(groups * a.cblocks)), dim3(64 * kWaves), 0, (hipStream_t)stream, a);
+    return launched("causal convolution, listed blocks");
+  }
   if (!token) {
-    const int64_t blocks = (int64_t)a.cblocks * a.tiles * p->seqs;
-    if (const rsq_status s = check_blocks(blocks, 64 * kWaves)) return s;
     hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * kWaves), 0, (hipStream_t)stream, a);
     return launched("causal convolution");
   }

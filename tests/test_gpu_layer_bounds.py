@@ -1,5 +1,6 @@
 """Layer operators where the bounds of their plain comparison leave room: results held to what their arithmetic leaves."""
 import numpy as np
+import numpy as np
 import pytest
 import torch
 
@@ -121,3 +122,52 @@ def test_scan_falling_offsets_of_long_sequences():
     y, got = rsq.ssm_scan(x, dt, A, B, C, D=D, dt_bias=bias, softplus=True, offsets=off, max_len=n)
     check(got, S, bS, "state")
     assert torch.isfinite(y).all()
+
+
+def conv_bounded(C, width, lengths_or_offsets, n, longest, dtype, given):
+    """causal_conv within the reference's bounds, rows of no sequence untouched, states as they follow."""
+    off = torch.tensor(lengths_or_offsets, dtype=torch.int32).cuda()
+    o = off.tolist()
+    seqs = [(a, max(0, b - a)) for a, b in zip(o[:-1], o[1:])]
+    r = gen(C)
+    x, w, b = r(n, C, dtype=dtype), r(C, width) * 0.5, r(C)
+    st = r(len(seqs), C, width - 1, dtype=dtype) if given else None
+    want, new, bound = ref.conv(x, w, b, st, seqs, True, dtype)
+    out = torch.full(x.shape, 7.0, dtype=dtype, device="cuda")
+    y = rsq.causal_conv(x, w, b, state=st, offsets=off, max_len=longest, activation="silu", out=out)
+    inside = torch.zeros(n, dtype=torch.bool)
+    for a, m in seqs:
+        inside[a: a + m] = True
+    check(y[inside.cuda()], want[inside], bound[inside], "y")
+    assert (y[~inside.cuda()] == 7.0).all()
+    if given:
+        assert torch.equal(st.cpu().double(), new)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("C,width", [(520, 4), (37, 3)])
+@pytest.mark.parametrize("count", [40, 300, 1500])
+def test_conv_long_prompts_among_many(dtype, C, width, count):
+    """Long prompts at the front, in the middle and at the end of sequences of a few tokens or none."""
+    lengths = [n % 3 for n in range(count)]
+    lengths[0], lengths[count // 2], lengths[-1] = 900, 333, 700
+    o = 3 + np.concatenate([[0], np.cumsum(lengths)])
+    conv_bounded(C, width, o.tolist(), int(o[-1]) + 2, 900, dtype, count == 300)
+
+
+def test_conv_falling_offsets_of_long_sequences():
+    """Sequences over the same rows have more blocks than rows allow for; no state, so that all give the same rows."""
+    n = 3000
+    conv_bounded(64, 4, [0, n] * 40, n, n, F32, False)
+
+
+def test_conv_more_equal_sequences_than_workgroups():
+    """2^24 - 1 workgroups of 256 threads a launch: two tokens each, an element a lane."""
+    n = (1 << 24) + 3
+    x = torch.zeros(n, 2, 5, dtype=BF16, device="cuda")
+    r = gen(6)
+    w, b = r(5, 3), r(5)
+    some = torch.cat([torch.arange(0, 9), torch.arange((1 << 23) - 5, (1 << 23) + 5), torch.arange(n - 9, n)]).cuda()
+    x[some] = r(len(some), 2, 5, dtype=BF16)
+    y = rsq.causal_conv(x, w, b)
+    assert torch.equal(y[some], rsq.causal_conv(x[some], w, b))
