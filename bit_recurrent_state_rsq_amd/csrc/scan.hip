@@ -468,7 +468,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
       // c = n + f with n whole: 2^{c_t - c_s} = 2^{f_t} 2^{n_t - n_s} 2^{-f_s}.
       // Where the n are within kNear of their middle, powers of two shift them
       // into the factors of t and s; both ways give the same bits.
-      constexpr int kNear = 40;   // the products that the factors scale have 2^87 left
+      constexpr int kNear = 40;
       const double n = rint(cum);
       const float f = (float)(cum - n);
       const int whole = (int)n, mid = (int)rint(0.5 * last);
@@ -602,7 +602,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
       const int tt = 16 * wave + n16;   // this lane's token
       const int mid = __builtin_amdgcn_readfirstlane(lds_mid[par]);
       __builtin_amdgcn_sched_barrier(0);
-      // y = to_t (2^{n} S^T C + P X), n the middle's power or this token's own
+      const float to = lds_to[par][tt];
       const int power = mid == kWide ? lds_whole[par][tt] : mid;
       u32x4 pf[kL / 32][PY];
       // ---- P^T (rows s, columns t), two tiles (a k-step of y) at a time, up to
@@ -628,7 +628,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
             const int s0 = 32 * j2 + 16 * e;
             const f32x4 from = *reinterpret_cast<const f32x4*>(&lds_from[par][s0 + 4 * g]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[e][r] *= from[r];
+            for (int r = 0; r < 4; ++r) acc[e][r] *= from[r] * to;   // (one factor may be 2^40 where the other is 2^-40)
             if (mid == kWide) {
               const i32x4 n = *reinterpret_cast<const i32x4*>(&lds_whole[par][s0 + 4 * g]);
 #pragma unroll
@@ -664,12 +664,10 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
         for (int p = 0; p < PI; ++p) xf[j2][p] = read_tr8<kV>(lds_x + p * XB + 32 * j2 * TX::kBytes + (a_xtr ^ (wave << 5)));
       const Rows rY(y, yrow, t0, len);
       __builtin_amdgcn_sched_barrier(0);
-      // y = to_t (2^{n} S^T C + P X), n the middle's power or this token's own
-      float to[kL / 16];
 #pragma unroll
       for (int e = 0; e < kL / 16; ++e) {
-        to[e] = lds_to[par][16 * e + n16];
-        const float before = __builtin_amdgcn_ldexpf(1.f, mid == kWide ? lds_whole[par][16 * e + n16] : mid);
+        // e^{c_t} of the tokens
+        const float before = __builtin_amdgcn_ldexpf(lds_to[par][16 * e + n16], mid == kWide ? lds_whole[par][16 * e + n16] : mid);
 #pragma unroll
         for (int r = 0; r < 4; ++r) sc[e][r] *= before;
       }
@@ -698,7 +696,7 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
         }
         float out[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], sc[e][r] * to[e]);
+        for (int r = 0; r < 4; ++r) out[r] = __builtin_fmaf(Dh, xv[r], sc[e][r]);
         if (bad) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)

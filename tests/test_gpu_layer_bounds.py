@@ -171,3 +171,21 @@ def test_conv_more_equal_sequences_than_workgroups():
     x[some] = r(len(some), 2, 5, dtype=BF16)
     y = rsq.causal_conv(x, w, b)
     assert torch.equal(y[some], rsq.causal_conv(x[some], w, b))
+
+
+# ---------------------------------------------------------------- the scan's range
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dk", [16, 128])
+def test_scan_large_products_of_b_and_c(dtype, dk):
+    """C . B of about 2^95 and x of 2^-80 under decays of 2^-76 a chunk: weights and outputs are in range throughout."""
+    n = 130
+    r = gen(dk)
+    x, B, C = r(n, 2, 16) * 2.0 ** -80, r(n, 1, dk) * 2.0 ** 55, r(n, 1, dk) * 2.0 ** 38
+    x, B, C = x.to(dtype), B.to(dtype), C.to(dtype)
+    dt = torch.full((n, 2), 0.825, device="cuda").to(dtype)
+    A = -torch.ones(2, device="cuda")
+    want, S, by, bS = ref.scan(x, dt, A, B, C, None, None, False, None, [(0, n)], dtype)
+    y, got = rsq.ssm_scan(x[None], dt[None], A, B[None], C[None])
+    check(y[0], want, by, "y")
+    check(got, S, bS, "state")
