@@ -452,12 +452,13 @@ __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2
   double total = 0.0;
   auto decays = [&](float dt, int t0, int par) {
     float delta = 0.f;
+    double cum = 0.;   // (not 0 A: A may be infinite)
     if (t0 + lane < len) {
       delta = dt + dt_bias;
       if (a.s.softplus) delta = softplus(delta);
+      cum = (double)delta * (double)A2;
     }
     // a token that decays by 2^-2000 keeps nothing of an fp32 state
-    double cum = (double)delta * (double)A2;
     cum = cum < -2000. ? -2000. : cum > 2000. ? 2000. : cum;
     cum = wave_scan(cum);
     const double last = lane63(cum);

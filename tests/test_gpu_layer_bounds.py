@@ -189,3 +189,22 @@ def test_scan_large_products_of_b_and_c(dtype, dk):
     y, got = rsq.ssm_scan(x[None], dt[None], A, B[None], C[None])
     check(y[0], want, by, "y")
     check(got, S, bS, "state")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 64, 100, 700])
+def test_scan_heads_that_keep_nothing(dtype, n):
+    """A of -inf: e^(delta A) is 0, so y is (C . B) delta x and the state what the last token adds, also where a chunk
+    is not full. 16 products and their sum, delta, the weight and its parts: at most 16 + 8 roundings of fp32."""
+    r = gen(n)
+    x, B, C = r(1, n, 2, 16, dtype=dtype), r(1, n, 1, 16, dtype=dtype), r(1, n, 1, 16, dtype=dtype)
+    dt = (r(1, n, 2).abs() + 0.1).to(dtype)
+    A = torch.tensor([-float("inf"), -1.0], device="cuda")
+    y, S = rsq.ssm_scan(x, dt, A, B, C)
+    xd, Bd, Cd, d = (t[0].cpu().double() for t in (x, B, C, dt))
+    want = (Cd * Bd).sum(2) * d[:, :1] * xd[:, 0]
+    mag = (Cd * Bd).abs().sum(2) * d[:, :1] * xd[:, 0].abs()
+    check(y[0, :, 0], want, mag * (24 * U + (2.0 ** -15 if dtype == BF16 else 0)) + 1.01 * ref.half_step(dtype) * want.abs())
+    last = Bd[-1, 0][:, None] * d[-1, 0] * xd[-1, 0][None]
+    check(S[0, 0], last, last.abs() * 8 * U)
+    assert torch.isfinite(y).all() and torch.isfinite(S).all()
