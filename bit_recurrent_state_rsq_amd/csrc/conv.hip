@@ -375,7 +375,7 @@ extern "C" rsq_status rsq_causal_conv(const rsq_conv* p, void* stream) {
   const Span read[] = {{p->x, span_bytes(p->tokens, p->x_stride, C, size), "x"},
                        {p->weight, C * p->width * 4, "weight"},
                        {p->bias, C * 4, "bias"},
-                       {p->offsets, (int64_t)(p->seqs + 1) * 4, "offsets"}};
+                       {p->offsets, ((int64_t)p->seqs + 1) * 4, "offsets"}};
   if (const rsq_status s = check_overlap(written, read)) return s;
 
   // 16-byte accesses where every row, parameter and state address allows them

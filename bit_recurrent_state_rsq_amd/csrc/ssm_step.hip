@@ -59,7 +59,7 @@ rsq_status check_ssm_memory(const rsq_ssm* p) {
                        {p->A, hb, "A"},
                        {p->D, hb, "D"},
                        {p->dt_bias, hb, "dt_bias"},
-                       {p->offsets, (int64_t)(p->seqs + 1) * 4, "offsets"}};
+                       {p->offsets, ((int64_t)p->seqs + 1) * 4, "offsets"}};
   return check_overlap(written, read);
 }
 

@@ -7,7 +7,7 @@ import pytest
 rsq = pytest.importorskip("bit_recurrent_state_rsq_amd")
 from bit_recurrent_state_rsq_amd import _abi  # noqa: E402
 from bit_recurrent_state_rsq_amd._abi import lib  # noqa: E402
-from test_layer_refusals import SSM, UNSUPPORTED, addr, fill  # noqa: E402
+from test_layer_refusals import CONV, INVALID, SSM, UNSUPPORTED, addr, fill  # noqa: E402
 
 
 def ssm(seqs, heads, max_len=1, d_v=8, **kw):
@@ -46,3 +46,12 @@ def test_scan_workspace_goes_by_the_segments_that_exist(seqs, tokens, max_len):
     n = ctypes.c_size_t()
     assert lib.rsq_ssm_scan_workspace(ctypes.byref(p), ctypes.byref(n)) == 0
     assert 0 < n.value <= 3 * 768 * (128 * 64 * 4 + 4)
+
+
+def test_outputs_over_the_offsets_of_the_most_sequences():
+    """2^31 - 1 sequences have 2^31 offsets: their bytes do not pass for none."""
+    most, far = 0x7FFFFFFF, 1 << 44
+    c = fill(_abi.Conv, {**CONV, "seqs": most, "state": None, "offsets": addr(4), "y": addr(4)})
+    assert lib.rsq_causal_conv(ctypes.byref(c), None) == INVALID
+    p = ssm(most, 1, max_len=10, tokens=20, offsets=addr(4), state=far, y=addr(4))
+    assert lib.rsq_ssm_scan(ctypes.byref(p), None) == INVALID
