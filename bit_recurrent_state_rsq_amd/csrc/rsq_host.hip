@@ -711,11 +711,8 @@ rsq_status rsq_decode_ssm_step(rsq_state* st, const rsq_ssm* p, void* stream) {
     return fail(RSQ_E_INVALID, "workspace is NULL or not 256-byte aligned");
   if (p->workspace_bytes < w.total)
     return fail(RSQ_E_BUFFER, "workspace has %zu bytes, the step needs %zu", p->workspace_bytes, w.total);
-  const int size = p->dtype == RSQ_BF16 ? 2 : 4;
   const rsq::Span buf{st->buf, (int64_t)st->layout.total, "state"};
-  const rsq::Span y{p->y, rsq::span_bytes(p->tokens, p->y_stride, (int64_t)p->heads * p->d_v, size), "y"};
-  if (rsq::overlap(buf, y) || rsq::overlap(buf, {p->workspace, (int64_t)p->workspace_bytes, "workspace"}))
-    return fail(RSQ_E_INVALID, "y or workspace overlaps the state's buffer");
+  if (const rsq_status s = rsq::check_ssm_apart(p, buf)) return s;
   if (st->bypass && st->n >= st->cap)
     return fail(RSQ_E_BYPASS_FULL, "bypass holds %d of %d columns: call rsq_merge_bypass", st->n, st->cap);
   if (st->bypass) {

@@ -64,6 +64,8 @@ namespace rsq {
 rsq_status check_ssm(const rsq_ssm* p, bool prompt);
 // Pointers: present, aligned, outputs apart from everything else.
 rsq_status check_ssm_memory(const rsq_ssm* p);
+// A written range outside the arguments is apart from all of them.
+rsq_status check_ssm_apart(const rsq_ssm* p, const Span& written);
 SsmArgs ssm_args(const rsq_ssm* p);
 
 // The decode step's inputs of one token: q and k from the head's C and B, v =

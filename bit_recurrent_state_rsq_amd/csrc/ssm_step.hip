@@ -38,6 +38,31 @@ rsq_status check_ssm(const rsq_ssm* p, bool prompt) {
   return RSQ_OK;
 }
 
+namespace {
+
+// the memory that a call writes and reads, but for its state
+int64_t ssm_span(const rsq_ssm* p, int64_t stride, int64_t cols) {
+  return span_bytes(p->tokens, stride, cols, p->dtype == RSQ_BF16 ? 2 : 4);
+}
+Span y_span(const rsq_ssm* p) { return {p->y, ssm_span(p, p->y_stride, (int64_t)p->heads * p->d_v), "y"}; }
+Span work_span(const rsq_ssm* p) { return {p->workspace, (int64_t)p->workspace_bytes, "workspace"}; }
+struct ReadSpans {
+  Span s[8];
+};
+ReadSpans read_spans(const rsq_ssm* p) {
+  const int64_t gk = (int64_t)p->groups * p->d_k, hb = (int64_t)p->heads * 4;
+  return {{{p->x, ssm_span(p, p->x_stride, (int64_t)p->heads * p->d_v), "x"},
+           {p->B, ssm_span(p, p->b_stride, gk), "B"},
+           {p->C, ssm_span(p, p->c_stride, gk), "C"},
+           {p->dt, ssm_span(p, p->dt_stride, p->heads), "dt"},
+           {p->A, hb, "A"},
+           {p->D, hb, "D"},
+           {p->dt_bias, hb, "dt_bias"},
+           {p->offsets, ((int64_t)p->seqs + 1) * 4, "offsets"}}};
+}
+
+}  // namespace
+
 rsq_status check_ssm_memory(const rsq_ssm* p) {
   const int size = p->dtype == RSQ_BF16 ? 2 : 4;
   if (p->tokens > 0 && (!p->x || !p->B || !p->C || !p->dt || !p->y))
@@ -48,19 +73,13 @@ rsq_status check_ssm_memory(const rsq_ssm* p) {
   if (!aligned(p->dt, size) || !aligned(p->A, 4) || !aligned(p->D, 4) || !aligned(p->dt_bias, 4) ||
       !aligned(p->offsets, 4))
     return fail(RSQ_E_INVALID, "a pointer is not aligned to its element type");
-  const int64_t hv = (int64_t)p->heads * p->d_v, gk = (int64_t)p->groups * p->d_k, hb = (int64_t)p->heads * 4;
-  const Span written[] = {{p->y, span_bytes(p->tokens, p->y_stride, hv, size), "y"},
-                          {p->state, (int64_t)p->seqs * p->d_k * hv * 4, "state"},
-                          {p->workspace, (int64_t)p->workspace_bytes, "workspace"}};
-  const Span read[] = {{p->x, span_bytes(p->tokens, p->x_stride, hv, size), "x"},
-                       {p->B, span_bytes(p->tokens, p->b_stride, gk, size), "B"},
-                       {p->C, span_bytes(p->tokens, p->c_stride, gk, size), "C"},
-                       {p->dt, span_bytes(p->tokens, p->dt_stride, p->heads, size), "dt"},
-                       {p->A, hb, "A"},
-                       {p->D, hb, "D"},
-                       {p->dt_bias, hb, "dt_bias"},
-                       {p->offsets, ((int64_t)p->seqs + 1) * 4, "offsets"}};
-  return check_overlap(written, read);
+  const Span written[] = {y_span(p), {p->state, (int64_t)p->seqs * p->d_k * p->heads * p->d_v * 4, "state"}, work_span(p)};
+  return check_overlap(written, read_spans(p).s);
+}
+
+rsq_status check_ssm_apart(const rsq_ssm* p, const Span& range) {
+  const Span written[] = {range, y_span(p), work_span(p)};
+  return check_overlap(written, read_spans(p).s);
 }
 
 SsmArgs ssm_args(const rsq_ssm* p) {

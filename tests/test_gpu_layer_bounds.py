@@ -208,3 +208,20 @@ def test_scan_heads_that_keep_nothing(dtype, n):
     last = Bd[-1, 0][:, None] * d[-1, 0] * xd[-1, 0][None]
     check(S[0, 0], last, last.abs() * 8 * U)
     assert torch.isfinite(y).all() and torch.isfinite(S).all()
+
+
+# ---------------------------------------------------------------- the step on a quantized state
+
+def test_state_step_refuses_operands_in_the_states_buffer():
+    st = rsq.State(model="mamba2", batch=2, heads=4, d_k=128, d_v=64, group=64, bits=8, in_dtype="bf16")
+    x, dt, A, B, C, D, bias = ssm_case(2, 4, 2, 128, 64, BF16, slices=False)
+    st.load_dense(gen(1)(2, 4, 128, 64))
+    before = st.buf.clone()
+    part = lambda t: st.buf[8192: 8192 + t.numel() * t.element_size()].view(t.dtype).view(t.shape)  # noqa: E731
+    for i in range(8):
+        args = [x, dt, A, B, C, D, bias, torch.empty_like(x)]
+        args[i] = part(args[i])
+        with pytest.raises(rsq.Error) as e:
+            st.ssm_step(*args[:5], D=args[5], dt_bias=args[6], softplus=True, out=args[7])
+        assert e.value.code == rsq._abi.RSQ_E_INVALID
+    assert torch.equal(st.buf, before) and st.counters() == (0, 0)
