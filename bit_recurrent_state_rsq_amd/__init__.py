@@ -260,6 +260,7 @@ class State:
         p = self._ptr(dense, torch.float32, shape, "dense")
         with _layer.on(dense.get_device(), stream) as s:
             check(lib.rsq_state_load(self.h, p, s))
+        _layer.record(stream, dense, self.buf)
 
     def ssm_step(self, x, dt, A, B, C, D=None, dt_bias=None, softplus=False, out=None, stream=None):
         """One token of a Mamba2 layer on this state (rsq_decode_ssm_step): the arguments of the

@@ -7,7 +7,9 @@ argument); the arithmetic runs in the HIP kernels. Activations are fp32 or
 bf16 tensors on one device, parameters fp32. Calls go to `stream` (default: the
 device's current stream) and can be captured in a graph; a tensor argument's
 rows may be strided, its elements within a row are contiguous. A tensor that a
-call makes belongs to the stream the call ran on.
+call makes belongs to the stream the call ran on. With `stream` given, the caller
+makes it wait for what the operands' own stream still does to them; they are
+recorded on it, so that they may be dropped once the call has returned.
 
     y = causal_conv(xbc, weight, bias, state=conv_state, activation="silu")
     y, S = ssm_scan(x, dt, A, B, C, D=D, dt_bias=dt_bias, softplus=True)     # a prompt
@@ -69,7 +71,17 @@ def _run(call, x, stream, *args):
     if stream is None and index >= 0 and _current_device() == index:
         return call(_raw_stream(index), *args)
     with on(index, stream) as s:
-        return call(s, *args)
+        made = call(s, *args)
+    record(stream, *args)
+    return made
+
+
+def record(stream, *operands):
+    """The tensors among the operands are in use on `stream` (where one is given) until its work so far is done."""
+    if stream is not None:
+        for t in operands:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
 
 
 def _choice(table, key, name):
@@ -122,7 +134,9 @@ def state_ssm_step(st, x, dt, A, B, C, D, dt_bias, softplus, out, stream):
     """State.ssm_step."""
     if x.device != st.device:
         raise ValueError("x must be on %s, got %s" % (st.device, x.device))
-    return _run(_binding.state_step, x, stream, st.h.value, x, dt, A, B, C, D, dt_bias, softplus, out)
+    y = _run(_binding.state_step, x, stream, st.h.value, x, dt, A, B, C, D, dt_bias, softplus, out)
+    record(stream, st.buf)
+    return y
 
 
 def rms_norm(x, weight, eps=1e-5, residual=None, out_dtype=None, group=0, out=None, scales=None, stream=None):
@@ -162,6 +176,7 @@ class W4Weight:
             self.packed = codes.new_empty(need.value, dtype=torch.uint8)
             check(lib.rsq_w4_pack(codes.data_ptr(), scales.data_ptr(), self.n, self.k, self.group, self.scale_dtype,
                                   self.packed.data_ptr(), need.value, s))
+        record(stream, codes, scales)
 
 
 def w4_linear(x, weight, x_scale=None, out_dtype=None, out=None, stream=None):

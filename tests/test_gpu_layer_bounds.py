@@ -225,3 +225,48 @@ def test_state_step_refuses_operands_in_the_states_buffer():
             st.ssm_step(*args[:5], D=args[5], dt_bias=args[6], softplus=True, out=args[7])
         assert e.value.code == rsq._abi.RSQ_E_INVALID
     assert torch.equal(st.buf, before) and st.counters() == (0, 0)
+
+
+# ---------------------------------------------------------------- streams
+
+def test_operands_dropped_while_another_stream_has_yet_to_read_them():
+    """stream=: the operands' memory is not given to the current stream's next tensors before the call has run."""
+    side = torch.cuda.Stream()
+    x, dt, A, B, C, D, bias = ssm_case(512, 2, 1, 64, 64, BF16, slices=False)
+    r = gen(9)
+    w, nw, cols = r(128, 4), r(128), r(512, 128, dtype=BF16)
+    codes, scales, _, _ = w4_case(1, 64, 128, 64, BF16, torch.float16)
+    given = r(1, 2, 64, 64)
+    opt = dict(D=D, dt_bias=bias, softplus=True)
+    w4 = rsq.W4Weight(codes, scales)
+    token = [t[:1].clone() for t in (x, dt, B, C)]
+
+    def quantized(dense, stream):
+        st = rsq.State(model="mamba2", batch=1, heads=2, d_k=128, d_v=64, group=64, bits=8, in_dtype="bf16")
+        torch.cuda.current_stream().synchronize()
+        st.load_dense(dense, stream=stream)
+        return st.buf
+
+    calls = [
+        (lambda v, s: rsq.causal_conv(v[0], w, stream=s), [cols[None]]),
+        (lambda v, s: rsq.causal_conv_step(v[0], w, stream=s), [cols]),
+        (lambda v, s: rsq.ssm_scan(v[0], v[1], A, v[2], v[3], stream=s, **opt)[0], [x[None], dt[None], B[None], C[None]]),
+        (lambda v, s: rsq.ssm_step(v[4], v[0], v[1], A, v[2], v[3], stream=s, **opt), token + [given]),
+        (lambda v, s: rsq.rms_norm(v[0], nw, stream=s), [cols]),
+        (lambda v, s: rsq.w4_linear(v[0], w4, stream=s), [cols]),
+        (lambda v, s: rsq.W4Weight(v[0], v[1], stream=s).packed, [codes, scales]),
+        (lambda v, s: quantized(v[0], s), [r(1, 2, 128, 64)]),
+    ]
+    for call, operands in calls:
+        want = call([t.clone() for t in operands], None)
+        mine = [t.clone() for t in operands]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = call(mine, side)
+        sizes = [(t.shape, t.dtype) for t in mine]
+        del mine
+        over = [torch.full(s, 3, dtype=d, device="cuda") for s, d in sizes for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del over
