@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import layer_reference as ref
+from layer_bounds import w4_norm_limit
 from layer_reference import H, U, check
 from test_gpu_layer import BF16, F32, gen, offsets_of, ssm_case, w4_case
 
@@ -270,3 +271,42 @@ def test_operands_dropped_while_another_stream_has_yet_to_read_them():
         torch.cuda.synchronize()
         assert torch.equal(got, want)
         del over
+
+
+# ---------------------------------------------------------------- 4-bit weights
+
+@pytest.mark.parametrize("xt", [F32, BF16, "e4m3", "int8"])
+@pytest.mark.parametrize("mean", [0.0, 1.0])
+@pytest.mark.parametrize("m,n,k,group", [(16, 512, 4736, 128), (3, 100, 1280, 32), (59, 705, 3712, 64), (70, 5500, 512, 128),
+                                         (40, 6100, 1024, 32)])
+def test_w4_norm_of_the_error(xt, mean, m, n, k, group):
+    """The error's norm within what the sums' roundings leave (layer_bounds), where the elementwise bound has room for
+    a lost piece of x."""
+    codes, s, x, xs = w4_case(m, n, k, group, xt, F32, seed=k)
+    if mean:
+        if xs is None:
+            x = (x.float() + mean).to(x.dtype)
+        else:
+            v = (x.float() * xs + mean)
+            xs = (v.abs().amax(1, keepdim=True) / (127 if xt == "int8" else 448)).contiguous()
+            x = torch.round(v / xs).to(torch.int8) if xt == "int8" else (v / xs).to(torch.float8_e4m3fn)
+    y = rsq.w4_linear(x, rsq.W4Weight(codes, s), x_scale=xs, out_dtype="f32").cpu().double().numpy()
+    c, sd, xd = codes.cpu().double().numpy(), s.cpu().double().numpy(), x.float().cpu().double().numpy()
+    if xs is not None:
+        xd = xd * xs.cpu().double().numpy()
+    want = xd @ (c * sd.repeat(group, 1)).T
+    if xt == "int8":      # exact inside a group: only y's own roundings are left
+        limit = 2 * U * np.sqrt((k // group / 4 + 8 + 3) / 3) * np.linalg.norm(want)
+    else:
+        limit = w4_norm_limit(c, sd, xd, group, xt is F32, xs is not None)
+    assert np.linalg.norm(y - want) <= limit
+
+
+@pytest.mark.parametrize("xt", [F32, BF16, "e4m3", "int8"])
+@pytest.mark.parametrize("m,n,k,group", [(16, 8512, 2048, 128), (64, 4096, 1024, 32), (1, 28672, 1024, 64)])
+def test_w4_is_repeatable(xt, m, n, k, group):
+    codes, s, x, xs = w4_case(m, n, k, group, xt, F32, seed=1)
+    w = rsq.W4Weight(codes, s)
+    first = rsq.w4_linear(x, w, x_scale=xs, out_dtype="f32")
+    for _ in range(8):
+        assert torch.equal(rsq.w4_linear(x, w, x_scale=xs, out_dtype="f32"), first)
