@@ -310,3 +310,80 @@ def test_w4_is_repeatable(xt, m, n, k, group):
     first = rsq.w4_linear(x, w, x_scale=xs, out_dtype="f32")
     for _ in range(8):
         assert torch.equal(rsq.w4_linear(x, w, x_scale=xs, out_dtype="f32"), first)
+
+
+# ---------------------------------------------------------------- the scan cut into segments
+
+def workspace_of(tokens, seqs, longest, heads, groups, dk, dv, dtype):
+    """Bytes that ssm_scan asks for."""
+    import ctypes
+    abi = rsq._abi
+    p = abi.Ssm()
+    kw = dict(dtype=abi.BF16 if dtype == BF16 else abi.F32, seqs=seqs, heads=heads, groups=groups, d_k=dk, d_v=dv,
+              tokens=tokens, max_len=longest, offsets=16, x_stride=heads * dv, y_stride=heads * dv, b_stride=groups * dk,
+              c_stride=groups * dk, dt_stride=heads)
+    for k, v in kw.items():
+        setattr(p, k, v)
+    n = ctypes.c_size_t()
+    rsq._abi.check(rsq._abi.lib.rsq_ssm_scan_workspace(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+@pytest.mark.parametrize("heads,groups,dk,dv,dtype", [(3, 1, 128, 72, BF16), (2, 2, 256, 136, BF16), (4, 2, 64, 200, BF16),
+                                                      (3, 1, 128, 136, F32), (4, 4, 64, 72, F32), (5, 1, 72, 8, F32)])
+@pytest.mark.parametrize("given", [True, False])
+def test_scan_segments_of_every_head_and_column_block(heads, groups, dk, dv, dtype, given):
+    lengths = [700, 5, 0, 300, 256]
+    n = sum(lengths)
+    assert workspace_of(n, 5, 700, heads, groups, dk, dv, dtype) > 0
+    case = ssm_case(n, heads, groups, dk, dv, dtype, seed=dk + dv)
+    off, _ = offsets_of(lengths)
+    seqs = [(int(a), m) for a, m in zip(off[:-1].tolist(), lengths)]
+    scan_bounded(case, off, seqs, gen(2)(5, heads, dk, dv) if given else None, 700)
+
+
+@pytest.mark.parametrize("heads,dk,dtype", [(64, 64, F32), (16, 128, F32), (64, 128, BF16), (16, 256, BF16)])
+def test_scan_repeats_to_the_bit(heads, dk, dtype):
+    """Kernels of every type and width, with the chip full: a result read before its product is done would differ."""
+    n = 2500
+    case = ssm_case(n, heads, 1, dk, 64, dtype, seed=5)
+    off, _ = offsets_of([1500, 7, 993])
+    args = (*case[:5], case[5], case[6], True, None, off, 1500)
+    y0, S0 = rsq.ssm_scan(*args)
+    assert torch.isfinite(y0).all()
+    for _ in range(10):
+        y, S = rsq.ssm_scan(*args)
+        assert torch.equal(y, y0) and torch.equal(S, S0)
+
+
+# ---------------------------------------------------------------- the step on a quantized state, to the bit
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kw", [dict(bits=4), dict(bits=6), dict(bits=8), dict(bits=32), dict(head_bits=[8, 6, 4, 8]),
+                                dict(bits=4, hadamard=True), dict(bits=8, scale_mode="yoked"), dict(bits=4, lrb_k=2, lrb_m=6)])
+def test_state_step_is_the_gates_and_a_decode_step(kw, dtype):
+    """State.ssm_step gives what decode_step does with q = C, k = B, v = delta x rounded to the inputs' type and alpha =
+    e^(delta A), and D x on its output. The dense step shows the same alpha (on a state of ones, without inputs) and
+    delta x (on a zero state, with B = 1)."""
+    n, heads, groups, dk, dv = 2, 4, 2, 128, 64
+    full = dict(model="mamba2", batch=n, heads=heads, d_k=dk, d_v=dv, group=64, in_dtype="bf16" if dtype == BF16 else "f32", **kw)
+    a, b = rsq.State(**full), rsq.State(**full)
+    S = gen(6)(n, heads, dk, dv)
+    a.load_dense(S)
+    b.load_dense(S)
+    for t in range(3):
+        x, dt, A, B, C, D, bias = ssm_case(n, heads, groups, dk, dv, dtype, seed=t)
+        opt = dict(dt_bias=bias, softplus=True)
+        y = a.ssm_step(x, dt, A, B, C, D=D, **opt)
+        none, one = torch.zeros_like(B[..., :8]), torch.ones_like(B[..., :8])
+        decay = torch.ones(n, heads, 8, 8, device="cuda")
+        rsq.ssm_step(decay, torch.zeros_like(x[..., :8]).contiguous(), dt, A, none, none, **opt)
+        added = torch.zeros(n, heads, 8, dv, device="cuda")
+        rsq.ssm_step(added, x.contiguous(), dt, A, one, none, **opt)
+        per = heads // groups
+        o = b.decode_step(C.repeat_interleave(per, 1).contiguous(), B.repeat_interleave(per, 1).contiguous(),
+                          added[:, :, 0].to(dtype).contiguous(), alpha=decay[..., 0, 0].contiguous())
+        assert torch.equal(a.buf, b.buf)
+        # (the sum's 53 bits rounded to fp32 as one operation would)
+        want = (o.double() + D.double()[:, None] * x.double()).float().to(dtype)
+        assert torch.equal(y, want)
