@@ -131,7 +131,8 @@ def _load():
         "rsq_abi_version": (I32, []),
         "rsq_allocate_head_bits": (I32, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float), I32,
                                          ctypes.c_float, ctypes.POINTER(I32)]),
-        # struct arguments as addresses: the callers pass a packed struct's bytes
+        # struct arguments as addresses (Conv, Ssm, Norm and W4 mirror rsq.h for callers of the C ABI; the
+        # package's own calls fill the header's structs in _binding)
         "rsq_causal_conv": (I32, [P, P]),
         "rsq_ssm_scan_workspace": (I32, [P, ctypes.POINTER(SZ)]),
         "rsq_ssm_scan": (I32, [P, P]),

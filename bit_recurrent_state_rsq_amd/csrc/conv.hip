@@ -36,8 +36,8 @@ struct ConvArgs {
   int32_t per, last;        // listed blocks: how many a workgroup takes, and the last workgroup along them
 };
 
-// exp(-v) saturates to infinity for v below about -88, where silu(v) rounds to
-// -0. bf16 results take the hardware's exp2 and reciprocal (their errors, a few
+// exp(-v) saturates to infinity for v below about -88, and silu(v), there smaller
+// than 2^-120, becomes -0. bf16 results take the hardware's exp2 and reciprocal (their errors, a few
 // 2^-23, vanish in the rounding to 8 bits); fp32 ones the exact division.
 template <typename T>
 __device__ __forceinline__ float silu(float v) {

@@ -140,8 +140,8 @@ def state_ssm_step(st, x, dt, A, B, C, D, dt_bias, softplus, out, stream):
 
 
 def rms_norm(x, weight, eps=1e-5, residual=None, out_dtype=None, group=0, out=None, scales=None, stream=None):
-    """RMS norm of the rows of x [..., cols] (rsq_rms_norm), after x + residual,
-    which replaces the residual where one is given.
+    """RMS norm of the rows of x, [rows, cols] or [sequences, tokens, cols]
+    (rsq_rms_norm), after x + residual, which replaces the residual where one is given.
 
     out_dtype: 'f32' or 'bf16' (default: x's type) returns y; 'int8' or 'e4m3'
     returns (codes, scales), one fp32 scale a row, or per `group` columns."""
@@ -180,7 +180,8 @@ class W4Weight:
 
 
 def w4_linear(x, weight, x_scale=None, out_dtype=None, out=None, stream=None):
-    """x [..., k] times a W4Weight [n, k]: y [..., n] (rsq_w4_linear).
+    """x, [rows, k] or [sequences, tokens, k], times a W4Weight [n, k]: y [..., n]
+    (rsq_w4_linear).
 
     x: float32 or bfloat16, or int8 / float8_e4m3fn codes with x_scale (fp32, one
     a row, or [..., k / group] with the weight's group), as rms_norm returns

@@ -379,11 +379,12 @@ rsq_status rsq_causal_conv(const rsq_conv* conv, void* stream);
  * x, B, C, y and state are 16-byte aligned, the strides of x, B, C and y
  * multiples of 16 bytes; d_k and d_v are multiples of 8.
  * rsq_ssm_scan takes d_k <= 256 (bf16) or 128 (fp32), d_v <= 4096, max_len
- * below 2^31 - 4096, rows at most 2^24 bytes apart and seqs * heads *
- * ceil(d_v / 64) workgroups or more, below 2^24 (RSQ_E_UNSUPPORTED beyond). bf16:
- * S and the token weights enter y as two bf16 pieces each (2^-16 of its terms,
- * before y is rounded to bf16); the state itself is exact to fp32. An infinite or
- * NaN x makes its column NaN from its token on; earlier tokens are not touched.
+ * below 2^31 - 4096, rows at most 2^24 bytes apart and fewer than 2^24 workgroups
+ * (heads * ceil(d_v / 64) for each sequence, and for each segment of long ones;
+ * RSQ_E_UNSUPPORTED beyond). bf16: S and the token weights enter y as two bf16
+ * pieces each (2^-16 of its terms, before y is rounded to bf16); the state itself
+ * is exact to fp32. An infinite or NaN x makes its column NaN from its token on;
+ * earlier tokens are not touched.
  * rsq_ssm_step takes one row of every sequence: offsets NULL, max_len 1; d_v <=
  * 1024, d_k <= 4096; seqs * heads below 2^24 (RSQ_E_UNSUPPORTED beyond).
  */
@@ -443,6 +444,8 @@ rsq_status rsq_state_load(rsq_state* st, const float* dense, void* stream);
  *   group      0: a scale per row; 32, 64 or 128 dividing cols: one per group
  *   scales     device fp32 [rows][cols / group] (group 0: [rows]); NULL without codes
  *   cols       at most 32768
+ * The sum of the squares is fp32: a row of magnitudes above 2^63 / sqrt(cols), whose
+ * squares overflow, gives zeros.
  */
 typedef struct rsq_norm {
   int32_t dtype, out_dtype, cols, group;
