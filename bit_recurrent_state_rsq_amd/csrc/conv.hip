@@ -9,7 +9,7 @@
 // runs, and walks a tile of tokens with the last W - 1 inputs in registers; a tile
 // reads W - 1 rows again (from L2). The next kAhead rows are loaded while the
 // last ones are worked on, and kept as they come (bf16 pairs) until then: 16384 x
-// 4352 bf16 (286 MB) 68 us, 4.2 TB/s, where a large copy moves 4.7; loaded one
+// 4352 bf16 (286 MB) 68 us, 4.2 TB/s, where a large copy moves 4.9; loaded one
 // row at a time 98. 1531 x 1031 fp32, one element a lane, 6.0 us.
 #include <type_traits>
 

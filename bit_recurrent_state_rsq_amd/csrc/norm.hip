@@ -11,7 +11,7 @@
 // output: R threads own it, each kCols consecutive columns at a time, so that
 // a wavefront reads 1 KB runs of bf16. 16384 x 4096 bf16 with a residual (537 MB)
 // takes 98 us, 5.5 TB/s (a large copy, which misses the last-level cache more,
-// moves 4.7); 16 rows of 2048 to E4M3 are 5.9 us of latency: launch, one round of
+// moves 4.9); 16 rows of 2048 to E4M3 are 5.9 us of latency: launch, one round of
 // loads, two sums.
 #include <type_traits>
 

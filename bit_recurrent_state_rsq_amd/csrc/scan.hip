@@ -6,17 +6,20 @@
 //   S   <- e^{c_L} S0 + sum_s B_s (d_s e^{c_L - c_s} x_s)^T:
 // four small matrix products a chunk, on the matrix cores.
 //
-// Bytes and products would take 61 and 31 us of 16384 tokens (64 heads of 128 x
-// 64, bf16, 283 MB); it takes 196 (1.4 TB/s, 219 TFLOP/s counting the recurrence's
-// own 5 operations an element). What that goes to: the state is formed twice (first
-// for the segments' starts, a third of the time, then along with y) and from three bf16 pieces
-// each (two would make errors of 2e-6 of an exact fp32 state), so that the matrix
-// cores are busy for 32% of the cycles and the vector unit (splitting, weighting,
-// rounding and the diagonal's mask) for 50%, which three wavefronts a SIMD overlap
-// little; registers (168) and LDS (43.5 KB) keep a fourth out. Measured without
-// gain: C B^T made once for all heads of a group, decays of four chunks at a time
-// by four wavefronts (5% longer), raised priority for the products, remainders by
-// dot products, more of the segments' states on their way at once.
+// Bytes and products would take 57 and 27 us of 16384 tokens (64 heads of 128 x
+// 64, bf16, 283 MB); it takes 226 to 235 (by the card; 1.2 TB/s, 185 TFLOP/s counting
+// the recurrence's own 5 operations an element). What that goes to: the state is
+// formed twice (first for the segments' starts, a third of the time, then along with
+// y), from three bf16 pieces each (two would make errors of 2e-6 of an exact fp32
+// state), and it and the token weights enter y as two pieces. In the second pass the
+// vector unit (splitting, weighting, rounding and the diagonal's mask) is busy for 55%
+// of the cycles, LDS for 47 and the matrix cores for 31, which three wavefronts a
+// SIMD between four barriers a chunk overlap little; registers (168) and LDS (43.5
+// KB) keep a fourth out. Measured without gain: C B^T made once for all heads of a
+// group, decays of four chunks at a time by four wavefronts (5% longer), raised
+// priority for the products, remainders by dot products, more of the segments' states
+// on their way at once, P in LDS of its own (one barrier less), C laid out for wider
+// reads.
 // 333 fp32 tokens take 19 us, 9 of them two empty launches.
 #include <initializer_list>
 
@@ -306,8 +309,8 @@ __device__ __forceinline__ bool find_share(const ScanArgs& a, int unit, int lane
 // weighted x that enters the state (a state stays exact to fp32). Products of
 // pieces below 2^-24 are left out. bf16 outputs take PY = 2: y before its own
 // rounding is then off by 2^-16 of its terms. (One piece would leave 2^-8 of them,
-// as much as that rounding where the state makes up y; it took 198 us where two take
-// 228, 16384 tokens of 64 heads of 128 x 64.)
+// as much as that rounding where the state makes up y; it took 205 us where two take
+// 235, 16384 tokens of 64 heads of 128 x 64.)
 //
 // Shares of the four wavefronts: wavefront w owns the 16 columns 16 w of the state
 // and of y, and all of d_k, in registers over the whole segment; S enters y straight
@@ -825,9 +828,9 @@ struct ScanPlan {
 // Sequences are cut into segments that run side by side when heads and
 // sequences alone do not fill the chip: about `target` workgroups of equal
 // length, three for each of 256 compute units (16384 tokens of 64 heads of 128 x 64
-// bf16 205 us, with 512 217, with 1024 224, measured together), or two where d_k lets no third in
-// (8192 tokens of 64 heads of 256 x 64 bf16 179 us, with 768 201; of 16 heads of
-// 128 x 128 fp32 197, 230).
+// bf16 235 us, with 512 254, with 1024 251), or two where d_k lets no third in (8192
+// tokens of 64 heads of 256 x 64 bf16 198 us, with 768 222, with 256 286; of 16 heads
+// of 128 x 128 fp32 201, 230, 216).
 // A segment costs its chunks one and a half times (the states first), and one
 // step for each segment before it, about 1/7 of a chunk's time: with n chunks,
 // sqrt(n / 11) of them a segment is the shortest that pays, and two chunks are

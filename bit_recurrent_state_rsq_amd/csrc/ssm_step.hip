@@ -102,7 +102,7 @@ namespace {
 // thread owns four consecutive columns, so that rows are read in whole, and
 // every rows-th run of rows, kAhead of them in flight. The sums over the rows
 // meet in LDS in a fixed order. 128 sequences of 64 heads of 128 x 64 (539 MB) take
-// 107 us, 5.0 TB/s (a large copy moves 4.7); one sequence 5.3 us, where an empty
+// 106 us, 5.1 TB/s (a large copy moves 4.9); one sequence 5.3 us, where an empty
 // launch takes 4.6.
 constexpr int kAhead = 8;
 
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
 // Inputs of a decode step on a quantized state: a workgroup per head and
 // sequence. They are d_k + d_v elements a head against the d_k d_v of the state
 // that the step then moves: two launches more (these and the skip connection),
-// 56 us against 44 for the step alone (128 sequences, 64 heads of 128 x 64, INT8).
+// 41 us against 30 for the step alone (128 sequences, 64 heads of 128 x 64, INT8).
 template <typename T>
 __global__ __launch_bounds__(128) void ssm_gates_kernel(SsmArgs a, SsmGates o) {
   const int64_t tile = blockIdx.x;

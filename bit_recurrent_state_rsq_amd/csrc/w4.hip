@@ -3,8 +3,8 @@
 // for the projections around a decode step.
 //
 // Half a byte a weight against 2 M operations: bound by memory at few rows
-// (16 int8 rows x 28672 x 8192, 122 MB: 28.6 us, 4.3 TB/s, where a large copy
-// moves 4.7; 1 x 2048 x 4096 is 4.8 us of latency: launch, one round of loads, the
+// (16 int8 rows x 28672 x 8192, 122 MB: 27.9 us, 4.4 TB/s, where a large copy
+// moves 4.9; 1 x 2048 x 4096 is 4.8 us of latency: launch, one round of loads, the
 // join), from 32 on by making bf16 numbers of the codes, which the vector unit
 // does for each 16 x MT rows anew (64 rows of bf16 76 us).
 // The packed layout holds 16 rows x 128 columns in 1 KB, 16 bytes a lane of a
