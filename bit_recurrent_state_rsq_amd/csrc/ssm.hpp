@@ -69,7 +69,9 @@ rsq_status check_ssm_apart(const rsq_ssm* p, const Span& written);
 SsmArgs ssm_args(const rsq_ssm* p);
 
 // The decode step's inputs of one token: q and k from the head's C and B, v =
-// delta x rounded to the inputs' type, alpha = exp(delta A).
+// delta x rounded to the inputs' type (the decode step takes q, k and v of one
+// type; of bf16 inputs that is 2^-8 of what the token adds, where an 8-bit state's
+// own codes are steps of 2^-7 of their group's largest), alpha = exp(delta A).
 struct SsmGates {
   void* q;
   void* k;

@@ -7,7 +7,7 @@ import torch
 import layer_reference as ref
 from layer_bounds import w4_norm_limit
 from layer_reference import H, U, check
-from test_gpu_layer import BF16, F32, gen, offsets_of, ssm_case, w4_case
+from test_gpu_layer import BF16, F32, gen, offsets_of, same, ssm_case, w4_case
 
 pytestmark = pytest.mark.gpu
 
@@ -387,3 +387,25 @@ def test_state_step_is_the_gates_and_a_decode_step(kw, dtype):
         # (the sum's 53 bits rounded to fp32 as one operation would)
         want = (o.double() + D.double()[:, None] * x.double()).float().to(dtype)
         assert torch.equal(y, want)
+
+
+def test_stream_given_inside_a_capture():
+    """stream= of the capturing stream, operands dropped while the capture runs: replays give the eager result."""
+    x, dt, A, B, C, D, bias = ssm_case(700, 2, 1, 64, 64, BF16, slices=False)
+    w = gen(2)(64, 4)
+    want = rsq.ssm_scan(x[None], dt[None], A, B[None], C[None], D=D)[0].clone()
+    rows = rsq.causal_conv(want[:, :, 0].contiguous(), w)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s = torch.cuda.current_stream()
+        y, _ = rsq.ssm_scan(x[None], dt[None], A, B[None], C[None], D=D, stream=s)
+        part = y[:, :, 0].contiguous()
+        z = rsq.causal_conv(part, w, stream=s)
+        del part
+    for _ in range(4):
+        y.zero_(), z.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(y, want) and same(z, rows)      # (the state grows until it overflows)
+        torch.randn(1000, device="cuda").sum().item()
