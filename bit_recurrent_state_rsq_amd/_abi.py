@@ -37,7 +37,7 @@ EXPORTS = ["rsq_state_bytes", "rsq_state_alloc", "rsq_state_free", "rsq_state_la
            "rsq_readout", "rsq_get_status", "rsq_last_error", "rsq_abi_version", "rsq_allocate_head_bits",
            "rsq_causal_conv", "rsq_ssm_scan_workspace", "rsq_ssm_scan", "rsq_ssm_step", "rsq_rms_norm",
            "rsq_w4_bytes", "rsq_w4_pack", "rsq_w4_linear", "rsq_state_load", "rsq_decode_ssm_workspace",
-           "rsq_decode_ssm_step"]
+           "rsq_decode_ssm_step", "rsq_linear_attention_workspace", "rsq_linear_attention", "rsq_linear_attention_step"]
 
 
 class Config(ctypes.Structure):
@@ -81,6 +81,14 @@ class Ssm(ctypes.Structure):
                 + [("tokens", _I64), ("max_len", _I64), ("offsets", _P), ("x", _P), ("x_stride", _I64), ("B", _P),
                    ("b_stride", _I64), ("C", _P), ("c_stride", _I64), ("dt", _P), ("dt_stride", _I64), ("A", _P),
                    ("D", _P), ("dt_bias", _P), ("state", _P), ("y", _P), ("y_stride", _I64), ("workspace", _P),
+                   ("workspace_bytes", ctypes.c_size_t)])
+
+
+class LinearAttn(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("dtype", "seqs", "heads", "key_heads", "d_k", "d_v", "state_in")]
+                + [("tokens", _I64), ("max_len", _I64), ("offsets", _P), ("q", _P), ("q_stride", _I64), ("k", _P),
+                   ("k_stride", _I64), ("v", _P), ("v_stride", _I64), ("alpha", _P), ("alpha_stride", _I64), ("beta", _P),
+                   ("beta_stride", _I64), ("state", _P), ("o", _P), ("o_stride", _I64), ("workspace", _P),
                    ("workspace_bytes", ctypes.c_size_t)])
 
 
@@ -137,6 +145,9 @@ def _load():
         "rsq_ssm_scan_workspace": (I32, [P, ctypes.POINTER(SZ)]),
         "rsq_ssm_scan": (I32, [P, P]),
         "rsq_ssm_step": (I32, [P, P]),
+        "rsq_linear_attention_workspace": (I32, [P, ctypes.POINTER(SZ)]),
+        "rsq_linear_attention": (I32, [P, P]),
+        "rsq_linear_attention_step": (I32, [P, P]),
         "rsq_rms_norm": (I32, [P, P]),
         "rsq_w4_bytes": (I32, [I32, I32, I32, I32, ctypes.POINTER(SZ)]),
         "rsq_w4_pack": (I32, [P, P, I32, I32, I32, I32, P, SZ, P]),

@@ -29,6 +29,9 @@ struct Library {
   rsq_status (*state_step)(rsq_state*, const rsq_ssm*, void*);
   rsq_status (*norm)(const rsq_norm*, void*);
   rsq_status (*w4)(const rsq_w4*, void*);
+  rsq_status (*attention_workspace)(const rsq_linear_attn*, size_t*);
+  rsq_status (*attention)(const rsq_linear_attn*, void*);
+  rsq_status (*attention_step)(const rsq_linear_attn*, void*);
 } lib;
 PyObject* raise_status = nullptr;   // the package's check(): raises for a status
 
@@ -140,21 +143,21 @@ void call(F f) {
 
 // Sequences of x: [seqs, T, ...], or packed [tokens, ...] with offsets.
 template <typename P>
-void sequences(P& p, const at::Tensor& x, int inner, PyObject* offsets, PyObject* max_len, const Like& like) {
+void sequences(P& p, const at::Tensor& x, int inner, PyObject* offsets, PyObject* max_len, const Like& like, const char* name = "x") {
   const Dims n = x.sizes();
   const int lead = (int)n.size() - inner;
   const bool given = max_len != Py_None;
   const int64_t longest = given ? (int64_t)integer(max_len) : 0;
   int64_t seqs;
   if (offsets == Py_None) {
-    if (lead != 2) refuse("x must have shape [sequences, tokens, ...] without offsets, got " + text(n));
-    if (given && longest != n[1]) refuse("max_len is not the number of tokens a sequence of x has");
+    if (lead != 2) refuse(std::string(name) + " must have shape [sequences, tokens, ...] without offsets, got " + text(n));
+    if (given && longest != n[1]) refuse(std::string("max_len is not the number of tokens a sequence of ") + name + " has");
     seqs = n[0];
     p.tokens = n[0] * n[1];
     p.max_len = n[1];
     p.offsets = nullptr;
   } else {
-    if (lead != 1) refuse("x must have shape [tokens, ...] with offsets, got " + text(n));
+    if (lead != 1) refuse(std::string(name) + " must have shape [tokens, ...] with offsets, got " + text(n));
     const at::Tensor& o = tensor(offsets, "offsets");
     if (!(o.is_cuda() && o.get_device() == like.device && o.scalar_type() == at::kInt && o.dim() == 1 && o.size(0) > 1 &&
           o.is_contiguous()))
@@ -485,6 +488,116 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// alpha or beta: fp32, one value a row and head of v (alpha also one a head)
+const float* gate_of(PyObject* o, const at::Tensor& v, const Like& like, bool fixed, const char* name, int64_t& stride) {
+  stride = 0;
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  const Dims n = v.sizes();
+  const Dims rows(n.data(), n.size() - 1);
+  if (fixed && t.dim() == 1) {
+    check_tensor(t, like, at::kFloat, {rows.back()}, name);
+    need(t.stride(0) == 1 || t.size(0) == 1, "alpha must be contiguous");
+    return t.data_ptr<float>();
+  }
+  check_tensor(t, like, at::kFloat, rows, name);
+  stride = row_step(t, 1, name);
+  // (a row of its own for all tokens, as expand() makes)
+  if (stride != 0 || fixed) return t.data_ptr<float>();
+  refuse(std::string(name) + " must have a row of its own for each token");
+}
+
+// q, k, v, alpha, beta from a[0] on; seqs, tokens, max_len and offsets are set
+void attention_operands(rsq_linear_attn& p, const at::Tensor& v, const Like& like, PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q");
+  const at::Tensor& k = tensor(a[1], "k");
+  if (like.type != at::kFloat && like.type != at::kBFloat16)
+    refuse("v must be float32 or bfloat16, got " + std::string(c10::toString(like.type)));
+  p.dtype = act_type(like.type);
+  const Dims n = v.sizes();
+  const int lead = (int)n.size() - 2;
+  if (k.dim() != v.dim()) refuse("k must have shape [..., key heads, d_k], got " + text(k.sizes()));
+  const int64_t H = n[lead], dv = n[lead + 1], G = k.size(lead), dk = k.size(lead + 1);
+  p.heads = small(H, "heads"), p.d_v = small(dv, "d_v"), p.key_heads = small(G, "key heads"), p.d_k = small(dk, "d_k");
+  int64_t keys[4];
+  for (int i = 0; i < lead; ++i) keys[i] = n[i];
+  keys[lead] = G, keys[lead + 1] = dk;
+  const Dims keyed(keys, lead + 2);
+  check_tensor(q, like, like.type, keyed, "q");
+  check_tensor(k, like, like.type, keyed, "k");
+  p.q = q.data_ptr(), p.q_stride = row_step(q, 2, "q");
+  p.k = k.data_ptr(), p.k_stride = row_step(k, 2, "k");
+  p.v = v.data_ptr(), p.v_stride = row_step(v, 2, "v");
+  p.alpha = gate_of(a[3], v, like, true, "alpha", p.alpha_stride);
+  p.beta = gate_of(a[4], v, like, false, "beta", p.beta_stride);
+}
+
+// attention(stream, q, k, v, alpha, beta, state, offsets, max_len, out) -> (o, state)
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 10)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& v = tensor(a[3], "v");
+    const Like like(v);
+    if (v.dim() != 3 && v.dim() != 4) refuse("v must have shape [..., heads, d_v], got " + text(v.sizes()));
+    rsq_linear_attn p{};
+    sequences(p, v, 2, a[7], a[8], like, "v");
+    attention_operands(p, v, like, a + 1);
+    const int64_t shape[4] = {p.seqs, p.heads, p.d_k, p.d_v};
+    p.state_in = a[6] != Py_None;
+    at::Tensor state;
+    if (p.state_in) {
+      p.state = static_cast<float*>(param(a[6], like, at::kFloat, shape, "state"));
+      state = THPVariable_Unpack(a[6]);
+    } else {
+      state = at::empty(shape, v.options().dtype(at::kFloat).requires_grad(false));
+      p.state = state.data_ptr<float>();
+    }
+    at::Tensor out = output(a[9], v, like, like.type, v.sizes());
+    p.o = out.data_ptr(), p.o_stride = row_step(out, 2, "out");
+    size_t bytes = 0;
+    call([&] { return lib.attention_workspace(&p, &bytes); });
+    at::Tensor work;
+    if (bytes) {
+      // the call's stream owns it: it is reused there only
+      work = at::empty({(int64_t)bytes}, v.options().dtype(at::kByte).requires_grad(false));
+      p.workspace = work.data_ptr(), p.workspace_bytes = bytes;
+    }
+    void* s = stream_of(a[0]);
+    call([&] { return lib.attention(&p, s); });
+    PyObject* o = THPVariable_Wrap(std::move(out));
+    if (!o) return nullptr;
+    PyObject* st = a[6];
+    if (p.state_in) Py_INCREF(st);
+    else st = THPVariable_Wrap(std::move(state));
+    PyObject* r = st ? PyTuple_Pack(2, o, st) : nullptr;
+    Py_DECREF(o);
+    Py_XDECREF(st);
+    return r;
+  });
+}
+
+// attention_step(stream, state, q, k, v, alpha, beta, out)
+PyObject* attention_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& v = tensor(a[4], "v");
+    const Like like(v);
+    if (v.dim() != 3) refuse("v must have shape [sequences, heads, d_v], got " + text(v.sizes()));
+    rsq_linear_attn p{};
+    p.seqs = small(v.size(0), "sequences");
+    p.tokens = v.size(0), p.max_len = 1;
+    attention_operands(p, v, like, a + 2);
+    need(a[1] != Py_None, "state is required");
+    p.state = static_cast<float*>(param(a[1], like, at::kFloat, {p.seqs, p.heads, p.d_k, p.d_v}, "state"));
+    p.state_in = 1;
+    at::Tensor out = output(a[7], v, like, like.type, v.sizes());
+    p.o = out.data_ptr(), p.o_stride = row_step(out, 2, "out");
+    void* s = stream_of(a[0]);
+    call([&] { return lib.attention_step(&p, s); });
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
 // bind(check, addresses of the library's functions in Library's order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   constexpr Py_ssize_t kFunctions = sizeof(Library) / sizeof(void*);
@@ -505,6 +618,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(conv), FAST(scan), FAST(step), FAST(state_step), FAST(norm), FAST(w4),
+                         FAST(attention), FAST(attention_step),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -68,6 +68,12 @@ rsq_status check_ssm_memory(const rsq_ssm* p);
 rsq_status check_ssm_apart(const rsq_ssm* p, const Span& written);
 SsmArgs ssm_args(const rsq_ssm* p);
 
+// The scan with given decays: S = alpha S + B x^T, y = S^T C (A, dt, dt_bias and D are
+// not looked at, the other arguments have been checked). alpha: fp32 [tokens][heads], rows
+// alpha_stride apart (0: one row for all tokens), or NULL for 1.
+rsq_status decayed_scan_workspace(const rsq_ssm* p, size_t* bytes);
+rsq_status run_decayed_scan(const rsq_ssm* p, const float* alpha, int64_t alpha_stride, void* stream);
+
 // The decode step's inputs of one token: q and k from the head's C and B, v =
 // delta x rounded to the inputs' type (the decode step takes q, k and v of one
 // type; of bf16 inputs that is 2^-8 of what the token adds, where an 8-bit state's

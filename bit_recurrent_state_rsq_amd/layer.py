@@ -22,12 +22,13 @@ import torch
 from . import _abi, _binding
 from ._abi import check, lib
 
-__all__ = ["causal_conv", "causal_conv_step", "ssm_scan", "ssm_step", "rms_norm", "W4Weight", "w4_linear"]
+__all__ = ["causal_conv", "causal_conv_step", "ssm_scan", "ssm_step", "linear_attention", "linear_attention_step", "rms_norm",
+           "W4Weight", "w4_linear"]
 
 # _binding checks the operands, makes the outputs and calls the library
 _binding.bind(check, *[ctypes.cast(getattr(lib, "rsq_" + name), ctypes.c_void_p).value for name in (
     "causal_conv", "ssm_scan_workspace", "ssm_scan", "ssm_step", "decode_ssm_workspace", "decode_ssm_step", "rms_norm",
-    "w4_linear")])
+    "w4_linear", "linear_attention_workspace", "linear_attention", "linear_attention_step")])
 
 _ACTIVATIONS = {None: _abi.ACT_NONE, "none": _abi.ACT_NONE, "silu": _abi.ACT_SILU}
 _OUT = {None: -1, "f32": _abi.F32, "bf16": _abi.BF16, "int8": _abi.INT8, "e4m3": _abi.E4M3}
@@ -137,6 +138,24 @@ def state_ssm_step(st, x, dt, A, B, C, D, dt_bias, softplus, out, stream):
     y = _run(_binding.state_step, x, stream, st.h.value, x, dt, A, B, C, D, dt_bias, softplus, out)
     record(stream, st.buf)
     return y
+
+
+def linear_attention(q, k, v, alpha=None, beta=None, state=None, offsets=None, max_len=None, out=None, stream=None):
+    """Attention with a decay for each head over prompts (rsq_linear_attention); returns (o, state).
+
+    S = alpha S + k u^T with u = v, or with write strengths beta the delta rule u = beta (v - alpha S^T k); o = S^T q.
+    v: [sequences, tokens, heads, d_v] (or packed [tokens, ...] with offsets and max_len, as causal_conv); q, k:
+    [..., key heads, d_k], shared by heads / key heads each; alpha, beta: fp32 [..., heads], alpha also [heads] for all
+    tokens, or None for 1. state: fp32 [sequences, heads, d_k, d_v] to start from, updated in place; None starts from
+    zero and makes one. State.load_dense takes it for the decode step."""
+    return _run(_binding.attention, v, stream, q, k, v, alpha, beta, state, offsets, max_len, out)
+
+
+def linear_attention_step(state, q, k, v, alpha=None, beta=None, out=None, stream=None):
+    """One token of every sequence on a dense fp32 state [sequences, heads, d_k, d_v], updated in place
+    (rsq_linear_attention_step): v [sequences, heads, d_v], q, k [sequences, key heads, d_k], alpha, beta [sequences,
+    heads] as in linear_attention. Returns o of v's shape."""
+    return _run(_binding.attention_step, v, stream, state, q, k, v, alpha, beta, out)
 
 
 def rms_norm(x, weight, eps=1e-5, residual=None, out_dtype=None, group=0, out=None, scales=None, stream=None):

@@ -434,6 +434,62 @@ rsq_status rsq_decode_ssm_step(rsq_state* st, const rsq_ssm* ssm, void* stream);
 rsq_status rsq_state_load(rsq_state* st, const float* dense, void* stream);
 
 /*
+ * Attention with a decay for each head over prompts (RetNet, Mamba2 and, with beta,
+ * Gated DeltaNet rows of Table 1), on a dense fp32 state that rsq_state_load takes:
+ *   u_t = v_t, or with beta the delta rule u_t = beta_t (v_t - alpha_t S_{t-1}^T k_t)
+ *   S_t = alpha_t S_{t-1} + k_t u_t^T          (S: d_k x d_v)
+ *   o_t = S_t^T q_t
+ * for every head h; heads are split evenly over key_heads, and those of one share
+ * its q and k.
+ *   dtype      RSQ_F32 | RSQ_BF16: q, k, v, o
+ *   q, k       device [tokens][key_heads][d_k];  v, o device [tokens][heads][d_v]
+ *   alpha      device fp32 [tokens][heads], not negative; alpha_stride 0: [heads], the
+ *              same for all tokens; NULL: 1. An alpha of 0 clears the state
+ *   beta       device fp32 [tokens][heads]; NULL: no delta rule
+ *   state      device fp32 [seqs][heads][d_k][d_v], replaced by the state after
+ *              each sequence. state_in 0: start from zero, the contents are not
+ *              read; 1: start from the contents (an empty sequence keeps them)
+ *   workspace  rsq_linear_attention_workspace bytes, 16-byte aligned (prompts only;
+ *              NULL where that is 0): with beta up to 496 bytes a token and head.
+ *              Its contents need not be kept.
+ * q, k, v, o and state are 16-byte aligned, the strides of q, k, v and o multiples
+ * of 16 bytes; d_k and d_v are multiples of 8, d_v <= 4096.
+ * rsq_linear_attention takes d_k <= 256 (bf16) or 128 (fp32), max_len below 2^31 -
+ * 4096, rows at most 2^24 bytes apart and fewer than 2^24 workgroups (RSQ_E_UNSUPPORTED
+ * beyond). With beta, sequences must not share rows: where offsets fall, results are
+ * unspecified. bf16: S, u and the token weights enter o as two bf16 pieces each (2^-16
+ * of its terms, before o is rounded to bf16); the state itself is exact to fp32. A v
+ * that is not finite makes its column NaN from its token on, a k, alpha or beta (with
+ * beta given) the whole head; earlier tokens are not touched.
+ * rsq_linear_attention_step takes one row of every sequence: offsets NULL, max_len
+ * 1; d_k <= 256; alpha and beta [seqs][heads].
+ */
+typedef struct rsq_linear_attn {
+  int32_t dtype, seqs, heads, key_heads, d_k, d_v;
+  int32_t state_in;
+  int64_t tokens, max_len;
+  const int32_t* offsets;
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  const float* alpha;
+  int64_t alpha_stride;
+  const float* beta;
+  int64_t beta_stride;
+  float* state;
+  void* o;
+  int64_t o_stride;
+  void* workspace;
+  size_t workspace_bytes;
+} rsq_linear_attn;
+rsq_status rsq_linear_attention_workspace(const rsq_linear_attn* attn, size_t* bytes);
+rsq_status rsq_linear_attention(const rsq_linear_attn* attn, void* stream);
+rsq_status rsq_linear_attention_step(const rsq_linear_attn* attn, void* stream);
+
+/*
  * Root-mean-square norm of rows:
  *   h = x + residual (stored back to residual, rounded to dtype; residual NULL: h = x)
  *   y = h / sqrt(mean(h^2) + eps) * weight, of the fp32 h
