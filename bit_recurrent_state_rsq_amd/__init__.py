@@ -27,7 +27,7 @@ from .accounting import step_bytes_per_tile, workload_step_bytes, workload_merge
 __all__ = ["State", "Error", "state_bytes", "make_config", "step_bytes_per_tile",
            "workload_step_bytes", "workload_merge_bytes", "allocate_head_bits", "ErrorAccounting",
            "causal_conv", "causal_conv_step", "ssm_scan", "ssm_step", "linear_attention", "linear_attention_step",
-           "rms_norm", "W4Weight", "w4_linear"]
+           "rms_norm", "block_norm", "W4Weight", "w4_linear", "W8Weight", "w8_linear"]
 
 
 def make_config(model, batch, heads, d_k, d_v, group, bits=4, head_bits=None,
@@ -409,4 +409,5 @@ class State:
 from .diagnostics import ErrorAccounting  # noqa: E402
 from . import layer as _layer  # noqa: E402
 from .layer import (causal_conv, causal_conv_step, ssm_scan, ssm_step, linear_attention,  # noqa: E402
-                    linear_attention_step, rms_norm, W4Weight, w4_linear)
+                    linear_attention_step, rms_norm, block_norm, W4Weight, w4_linear, W8Weight,
+                    w8_linear)

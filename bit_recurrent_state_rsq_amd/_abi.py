@@ -28,7 +28,7 @@ SCALE_MODES = {"dynamic": SCALE_DYNAMIC, "persistent": SCALE_PERSISTENT, "yoked"
 F32, F16, BF16, INT8, E4M3 = 0, 1, 2, 3, 4
 DTYPES = {"f32": F32, "f16": F16, "bf16": BF16}
 INIT_ZERO, ATTACH = 0, 1
-ACT_NONE, ACT_SILU = 0, 1
+ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2
 F_NONFINITE, F_SCALE_OVERFLOW, F_CLIPPED = 1, 2, 4
 
 EXPORTS = ["rsq_state_bytes", "rsq_state_alloc", "rsq_state_free", "rsq_state_layout",
@@ -37,7 +37,8 @@ EXPORTS = ["rsq_state_bytes", "rsq_state_alloc", "rsq_state_free", "rsq_state_la
            "rsq_readout", "rsq_get_status", "rsq_last_error", "rsq_abi_version", "rsq_allocate_head_bits",
            "rsq_causal_conv", "rsq_ssm_scan_workspace", "rsq_ssm_scan", "rsq_ssm_step", "rsq_rms_norm",
            "rsq_w4_bytes", "rsq_w4_pack", "rsq_w4_linear", "rsq_state_load", "rsq_decode_ssm_workspace",
-           "rsq_decode_ssm_step", "rsq_linear_attention_workspace", "rsq_linear_attention", "rsq_linear_attention_step"]
+           "rsq_decode_ssm_step", "rsq_linear_attention_workspace", "rsq_linear_attention", "rsq_linear_attention_step",
+           "rsq_block_norm", "rsq_w8_bytes", "rsq_w8_pack", "rsq_w8_workspace", "rsq_w8_linear"]
 
 
 class Config(ctypes.Structure):
@@ -104,6 +105,21 @@ class W4(ctypes.Structure):
                    ("packed_bytes", ctypes.c_size_t), ("y", _P), ("y_stride", _I64)])
 
 
+class Block(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("dtype", "out_dtype", "cols", "group", "weight_cols", "scale_group", "activation",
+                                     "gate_first")]
+                + [("eps", _F), ("residual_scale", _F), ("rows", _I64), ("x", _P), ("x_stride", _I64), ("gate", _P),
+                   ("gate_stride", _I64), ("residual", _P), ("residual_stride", _I64), ("weight", _P), ("next_weight", _P),
+                   ("y", _P), ("y_stride", _I64), ("scales", _P)])
+
+
+class W8(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("out_dtype", "m", "n", "k")]
+                + [("x", _P), ("x_stride", _I64), ("x_scale", _P), ("bias", _P), ("packed", _P),
+                   ("packed_bytes", ctypes.c_size_t), ("y", _P), ("y_stride", _I64), ("workspace", _P),
+                   ("workspace_bytes", ctypes.c_size_t)])
+
+
 class Error(RuntimeError):
     def __init__(self, code, msg):
         super().__init__("rsq error %d: %s" % (code, msg))
@@ -139,7 +155,7 @@ def _load():
         "rsq_abi_version": (I32, []),
         "rsq_allocate_head_bits": (I32, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float), I32,
                                          ctypes.c_float, ctypes.POINTER(I32)]),
-        # struct arguments as addresses (Conv, Ssm, Norm and W4 mirror rsq.h for callers of the C ABI; the
+        # struct arguments as addresses (Conv, Ssm and the others mirror rsq.h for callers of the C ABI; the
         # package's own calls fill the header's structs in _binding)
         "rsq_causal_conv": (I32, [P, P]),
         "rsq_ssm_scan_workspace": (I32, [P, ctypes.POINTER(SZ)]),
@@ -149,6 +165,11 @@ def _load():
         "rsq_linear_attention": (I32, [P, P]),
         "rsq_linear_attention_step": (I32, [P, P]),
         "rsq_rms_norm": (I32, [P, P]),
+        "rsq_block_norm": (I32, [P, P]),
+        "rsq_w8_bytes": (I32, [I32, I32, ctypes.POINTER(SZ)]),
+        "rsq_w8_pack": (I32, [P, P, I32, I32, P, SZ, P]),
+        "rsq_w8_workspace": (I32, [P, ctypes.POINTER(SZ)]),
+        "rsq_w8_linear": (I32, [P, P]),
         "rsq_w4_bytes": (I32, [I32, I32, I32, I32, ctypes.POINTER(SZ)]),
         "rsq_w4_pack": (I32, [P, P, I32, I32, I32, I32, P, SZ, P]),
         "rsq_w4_linear": (I32, [P, P]),

@@ -40,7 +40,8 @@ FLAGS = [
 # accumulation registers (which the compiler picks for kernels of low occupancy)
 # it was seen to read them too early behind a branch.
 VGPR_RESULTS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-SOURCE_FLAGS = {"scan.hip": VGPR_RESULTS, "w4.hip": VGPR_RESULTS, "delta.hip": VGPR_RESULTS}
+SOURCE_FLAGS = {"scan.hip": VGPR_RESULTS, "w4.hip": VGPR_RESULTS, "delta.hip": VGPR_RESULTS,
+                "w8.hip": VGPR_RESULTS}
 
 
 def sources():

@@ -32,6 +32,9 @@ struct Library {
   rsq_status (*attention_workspace)(const rsq_linear_attn*, size_t*);
   rsq_status (*attention)(const rsq_linear_attn*, void*);
   rsq_status (*attention_step)(const rsq_linear_attn*, void*);
+  rsq_status (*block_norm)(const rsq_block*, void*);
+  rsq_status (*w8_workspace)(const rsq_w8*, size_t*);
+  rsq_status (*w8)(const rsq_w8*, void*);
 } lib;
 PyObject* raise_status = nullptr;   // the package's check(): raises for a status
 
@@ -598,6 +601,150 @@ PyObject* attention_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw std::runtime_error("");
+  return v;
+}
+
+// block_norm(stream, x, weight, gate, gate_first, activation, group, eps, residual, residual_scale, next_weight, out_type (-1:
+// x's, and no y where the residual is the result), scale_group, out, scales) -> y, (codes, scales) or the residual
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 15)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& x = tensor(a[1], "x");
+    const Like like(x);
+    rsq_block p{};
+    p.dtype = act_type(like.type);
+    const Dims dims = x.sizes();
+    if (dims.size() != 2 && dims.size() != 3)
+      refuse("x must have shape [rows, cols] or [sequences, tokens, cols], got " + text(dims));
+    const int64_t cols = dims.back();
+    const long t = integer(a[11]);
+    const at::ScalarType type = t < 0 ? like.type : out_type(t);
+    p.out_dtype = t < 0 ? p.dtype : (int32_t)t;
+    const bool codes = p.out_dtype == RSQ_INT8 || p.out_dtype == RSQ_E4M3;
+    p.cols = small(cols, "cols");
+    p.group = small(integer(a[6]), "group"), p.scale_group = small(integer(a[12]), "scale_group");
+    p.activation = (int32_t)integer(a[5]);
+    const int first = PyObject_IsTrue(a[4]);
+    if (first < 0) throw std::runtime_error("");
+    p.gate_first = first;
+    p.eps = (float)number(a[7]);
+    p.residual_scale = (float)number(a[9]);
+    p.rows = dims.size() == 2 ? dims[0] : dims[0] * dims[1];
+    p.x = x.data_ptr(), p.x_stride = row_step(x, 1, "x");
+    if (a[2] != Py_None) {
+      const at::Tensor& w = tensor(a[2], "weight");
+      const int64_t wc = p.group > 0 && w.dim() == 1 && w.size(0) == p.group ? p.group : cols;
+      p.weight = static_cast<const float*>(param(a[2], like, at::kFloat, {wc}, "weight"));
+      p.weight_cols = (int32_t)wc;
+    }
+    p.next_weight = static_cast<const float*>(param(a[10], like, at::kFloat, {cols}, "next_weight"));
+    if (a[3] != Py_None) {
+      const at::Tensor& g = tensor(a[3], "gate");
+      check_tensor(g, like, like.type, dims, "gate");
+      p.gate = g.data_ptr(), p.gate_stride = row_step(g, 1, "gate");
+    }
+    if (a[8] != Py_None) {
+      const at::Tensor& r = tensor(a[8], "residual");
+      check_tensor(r, like, like.type, dims, "residual");
+      p.residual = r.data_ptr(), p.residual_stride = row_step(r, 1, "residual");
+    }
+    // (an empty residual has no address: the operand itself says whether there is one)
+    const bool only = t < 0 && a[8] != Py_None && !p.next_weight && a[13] == Py_None;
+    at::Tensor out;
+    if (!only) {
+      out = output(a[13], x, like, type, dims);
+      p.y = out.data_ptr(), p.y_stride = row_step(out, 1, "out");
+    }
+    PyObject* sc = nullptr;
+    if (codes) {
+      int64_t shape[3];
+      const size_t lead = dims.size() - 1;
+      for (size_t i = 0; i < lead; ++i) shape[i] = dims[i];
+      shape[lead] = p.scale_group > 0 ? cols / p.scale_group : 1;
+      const Dims sdims(shape, lead + 1);
+      if (a[14] == Py_None) {
+        at::Tensor s = at::empty(sdims, x.options().dtype(at::kFloat).requires_grad(false));
+        p.scales = s.data_ptr<float>();
+        sc = THPVariable_Wrap(std::move(s));
+        if (!sc) return nullptr;
+      } else {
+        p.scales = static_cast<float*>(param(a[14], like, at::kFloat, sdims, "scales"));
+        Py_INCREF(sc = a[14]);
+      }
+    } else {
+      need(a[14] == Py_None, "scales go with an 8-bit output");
+    }
+    try {
+      void* s = stream_of(a[0]);
+      call([&] { return lib.block_norm(&p, s); });
+    } catch (...) {
+      Py_XDECREF(sc);
+      throw;
+    }
+    if (only) {
+      Py_INCREF(a[8]);
+      return a[8];
+    }
+    PyObject* y = THPVariable_Wrap(std::move(out));
+    if (!codes) return y;
+    PyObject* r = y ? PyTuple_Pack(2, y, sc) : nullptr;
+    Py_XDECREF(y);
+    Py_DECREF(sc);
+    return r;
+  });
+}
+
+// w8(stream, x, packed, n, k, x_scale, bias, out_type (-1: bf16), out)
+PyObject* w8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 9)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& x = tensor(a[1], "x");
+    const at::Tensor& packed = tensor(a[2], "weight");
+    const Like like(x);
+    if (like.type != at::kChar) refuse("x must be int8, got " + std::string(c10::toString(like.type)));
+    const Dims dims = x.sizes();
+    if (dims.size() != 2 && dims.size() != 3)
+      refuse("x must have shape [rows, k] or [sequences, tokens, k], got " + text(dims));
+    rsq_w8 p{};
+    p.n = (int32_t)integer(a[3]), p.k = (int32_t)integer(a[4]);
+    if (dims.back() != p.k) refuse("x must have as many columns as weight, got " + text(dims));
+    if (!(packed.is_cuda() && packed.get_device() == like.device)) refuse("weight and x must be on one device");
+    const size_t lead = dims.size() - 1;
+    p.m = small(lead == 1 ? dims[0] : dims[0] * dims[1], "rows");
+    p.x = static_cast<const int8_t*>(x.data_ptr()), p.x_stride = row_step(x, 1, "x");
+    need(a[5] != Py_None, "x_scale is required");
+    const Dims sd = tensor(a[5], "x_scale").sizes();
+    bool ok = sd.size() == lead || (sd.size() == lead + 1 && sd[lead] == 1);
+    for (size_t i = 0; ok && i < lead; ++i) ok = sd[i] == dims[i];
+    if (!ok) refuse("x_scale must have one value a row of x, got shape " + text(sd));
+    p.x_scale = static_cast<const float*>(param(a[5], like, at::kFloat, sd, "x_scale"));
+    p.bias = static_cast<const float*>(param(a[6], like, at::kFloat, {p.n}, "bias"));
+    const long t = integer(a[7]);
+    p.out_dtype = t >= 0 ? (int32_t)t : RSQ_BF16;
+    need(p.out_dtype == RSQ_F32 || p.out_dtype == RSQ_BF16, "out_dtype must be 'f32' or 'bf16'");
+    int64_t shape[3];
+    for (size_t i = 0; i < lead; ++i) shape[i] = dims[i];
+    shape[lead] = p.n;
+    at::Tensor out = output(a[8], x, like, out_type(p.out_dtype), Dims(shape, lead + 1));
+    p.y = out.data_ptr(), p.y_stride = row_step(out, 1, "out");
+    p.packed = packed.data_ptr(), p.packed_bytes = (size_t)packed.numel();
+    size_t bytes = 0;
+    call([&] { return lib.w8_workspace(&p, &bytes); });
+    at::Tensor work;
+    if (bytes) {
+      // the call's stream owns it: it is reused there only
+      work = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte).requires_grad(false));
+      p.workspace = work.data_ptr(), p.workspace_bytes = bytes;
+    }
+    void* s = stream_of(a[0]);
+    call([&] { return lib.w8(&p, s); });
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
 // bind(check, addresses of the library's functions in Library's order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   constexpr Py_ssize_t kFunctions = sizeof(Library) / sizeof(void*);
@@ -618,7 +765,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(conv), FAST(scan), FAST(step), FAST(state_step), FAST(norm), FAST(w4),
-                         FAST(attention), FAST(attention_step),
+                         FAST(attention), FAST(attention_step), FAST(block_norm), FAST(w8),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

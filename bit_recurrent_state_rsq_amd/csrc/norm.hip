@@ -16,13 +16,10 @@
 #include <type_traits>
 
 #include "host_util.hpp"
-#include "layer_ops.hpp"
+#include "norm.hpp"
 
 namespace rsq {
 namespace {
-
-constexpr int kCols = 8;   // consecutive columns of a thread
-enum { kOutF32, kOutBf16, kOutInt8, kOutE4m3 };
 
 struct NormArgs {
   const void* x;
@@ -36,64 +33,6 @@ struct NormArgs {
   float eps;
   int32_t wide;          // bit 0: x, 1: residual, 2: y, 3: weight take 16-byte (y: 8-byte codes) accesses
 };
-
-template <typename T>
-__device__ __forceinline__ void load_cols(const T* p, int c, int cols, bool wide, float (&v)[kCols]) {
-  if (wide && c + kCols <= cols) {
-    load_vec<kCols>(p + c, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < kCols; ++e) v[e] = c + e < cols ? to_f32(p[c + e]) : 0.f;
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_cols(T* p, int c, int cols, bool wide, const float (&v)[kCols]) {
-  if (wide && c + kCols <= cols) {
-    store_vec<kCols>(p + c, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < kCols; ++e)
-      if (c + e < cols) from_f32(v[e], p[c + e]);
-  }
-}
-
-__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
-// Sum (SUM) or the larger bit pattern over the R threads of a row, in a fixed
-// order: lanes 1, 2, ... apart, then the wavefronts of the row through LDS.
-template <int R, bool SUM>
-__device__ __forceinline__ uint32_t row_reduce(uint32_t v, uint32_t* lds) {
-  auto join = [](uint32_t a, uint32_t b) {
-    if constexpr (SUM) return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-    else return max_bits(a, b);
-  };
-#pragma unroll
-  for (int m = 1; m < (R < 64 ? R : 64); m <<= 1) v = join(v, (uint32_t)__shfl_xor((int)v, m, 64));
-  if constexpr (R > 64) {
-    constexpr int NW = R / 64;
-    __syncthreads();   // the last reduction's values have been read
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) v = join(v, lds[w]);
-  }
-  return v;
-}
-
-// code of y for the step `scale`: zero where the step is zero (or a NaN: the
-// scale then says so), clamped to the codes' range
-template <int OUT>
-__device__ __forceinline__ uint32_t encode(float y, float scale) {
-  const float v = scale == 0.f ? 0.f : y / scale;
-  if constexpr (OUT == kOutE4m3) {
-    return f32_to_e4m3(v);
-  } else {
-    const float r = rintf(fminf(fmaxf(v, -127.f), 127.f));
-    return v == v ? (uint32_t)(int)r & 0xFFu : 0u;
-  }
-}
 
 // R threads a row, up to NV * kCols columns a thread.
 template <typename T, int OUT, int R, int NV>
@@ -134,49 +73,7 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < kCols; ++e) h[i][e] = h[i][e] * rstd * w[e];
   }
-  if constexpr (OUT == kOutF32 || OUT == kOutBf16) {
-    typedef typename std::conditional<OUT == kOutF32, float, Bf16>::type O;
-    O* y = reinterpret_cast<O*>(a.y) + row * a.y_stride;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) store_cols(y, (i * R + tid) * kCols, a.cols, a.wide & 4, h[i]);
-  } else {
-    constexpr float qmax = OUT == kOutE4m3 ? 448.f : 127.f;
-    // absolute values order like their bit patterns, and a NaN's is the largest
-    uint32_t m[NV], all = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      m[i] = 0;
-#pragma unroll
-      for (int e = 0; e < kCols; ++e) m[i] = max_bits(m[i], __float_as_uint(h[i][e]) & 0x7FFFFFFFu);
-      all = max_bits(all, m[i]);
-    }
-    if (a.group == 0) all = row_reduce<R, false>(all, lds);
-    uint8_t* y = reinterpret_cast<uint8_t*>(a.y) + row * a.y_stride;
-    const int groups = a.group ? a.cols / a.group : 1;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * R + tid) * kCols;
-      uint32_t g = a.group ? m[i] : all;
-      // a group is group / kCols (4, 8 or 16) neighbouring lanes
-      if (a.group)
-        for (int s = 1; s < a.group / kCols; s <<= 1) g = max_bits(g, (uint32_t)__shfl_xor((int)g, s, 64));
-      const float scale = __uint_as_float(g) / qmax;
-      if (c < a.cols) {
-        if (a.group ? c % a.group == 0 : c == 0) a.scales[row * groups + (a.group ? c / a.group : 0)] = scale;
-        uint32_t q[kCols];
-#pragma unroll
-        for (int e = 0; e < kCols; ++e) q[e] = encode<OUT>(h[i][e], scale);
-        if ((a.wide & 4) && c + kCols <= a.cols) {
-          *reinterpret_cast<uint2*>(y + c) = make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
-                                                        q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kCols; ++e)
-            if (c + e < a.cols) y[c + e] = (uint8_t)q[e];
-        }
-      }
-    }
-  }
+  store_row<OUT, R, NV>(h, a.y, a.scales, row, a.y_stride, a.cols, a.group, a.wide & 4, tid, lds);
 }
 
 typedef void (*NormFn)(NormArgs);

@@ -1,6 +1,8 @@
 """Operators of the layer around the decode step: the short causal convolution,
-the selective state-space scan of prompts and its single-token step, the RMS
-norm with an 8-bit output, and products with 4-bit weights.
+the selective state-space scan of prompts and its single-token step, attention
+with a decay for each head (with or without the delta rule) of prompts and single
+tokens, norms around a block with 8-bit outputs, and products with 4-bit and 8-bit
+weights.
 
 Argument marshalling for the C ABI (include/rsq.h, which documents every
 argument); the arithmetic runs in the HIP kernels. Activations are fp32 or
@@ -23,14 +25,16 @@ from . import _abi, _binding
 from ._abi import check, lib
 
 __all__ = ["causal_conv", "causal_conv_step", "ssm_scan", "ssm_step", "linear_attention", "linear_attention_step", "rms_norm",
-           "W4Weight", "w4_linear"]
+           "block_norm", "W4Weight", "w4_linear", "W8Weight", "w8_linear"]
 
 # _binding checks the operands, makes the outputs and calls the library
 _binding.bind(check, *[ctypes.cast(getattr(lib, "rsq_" + name), ctypes.c_void_p).value for name in (
     "causal_conv", "ssm_scan_workspace", "ssm_scan", "ssm_step", "decode_ssm_workspace", "decode_ssm_step", "rms_norm",
-    "w4_linear", "linear_attention_workspace", "linear_attention", "linear_attention_step")])
+    "w4_linear", "linear_attention_workspace", "linear_attention", "linear_attention_step",
+    "block_norm", "w8_workspace", "w8_linear")])
 
 _ACTIVATIONS = {None: _abi.ACT_NONE, "none": _abi.ACT_NONE, "silu": _abi.ACT_SILU}
+_GATES = {**_ACTIVATIONS, "sigmoid": _abi.ACT_SIGMOID}
 _OUT = {None: -1, "f32": _abi.F32, "bf16": _abi.BF16, "int8": _abi.INT8, "e4m3": _abi.E4M3}
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
@@ -167,6 +171,23 @@ def rms_norm(x, weight, eps=1e-5, residual=None, out_dtype=None, group=0, out=No
     return _run(_binding.norm, x, stream, x, weight, eps, residual, _choice(_OUT, out_dtype, "out_dtype"), group, out, scales)
 
 
+def block_norm(x, weight=None, gate=None, gate_first=False, activation="silu", group=0, eps=1e-5, residual=None,
+               residual_scale=1.0, next_weight=None, out_dtype=None, scale_group=0, out=None, scales=None, stream=None):
+    """Norms before and after a block with its gate and residual, of the rows of x, [rows, cols] or [sequences, tokens,
+    cols] (rsq_block_norm):
+
+        u = rms_norm(x) * weight, over the row or each `group` columns; * act(gate) after it, or with gate_first before it
+        h = residual + residual_scale * u, which replaces the residual
+        y = rms_norm(h) * next_weight
+
+    Parts whose operand is None are left out. weight: fp32 [cols], or [group] for all groups; gate and residual like x;
+    activation: 'silu', 'sigmoid' or None. out_dtype: 'f32' or 'bf16' (default: x's type) returns y; 'int8' or 'e4m3'
+    returns (codes, scales), one fp32 scale a row, or per `scale_group` columns. With a residual and neither
+    next_weight, out_dtype nor out, the new residual is the result, and y is not written apart from it."""
+    return _run(_binding.block_norm, x, stream, x, weight, gate, gate_first, _choice(_GATES, activation, "activation"), group,
+                eps, residual, residual_scale, next_weight, _choice(_OUT, out_dtype, "out_dtype"), scale_group, out, scales)
+
+
 def _need(cond, fmt, *args):
     if not cond:
         raise ValueError(fmt % args)
@@ -206,4 +227,35 @@ def w4_linear(x, weight, x_scale=None, out_dtype=None, out=None, stream=None):
     a row, or [..., k / group] with the weight's group), as rms_norm returns
     them. out_dtype: 'f32' or 'bf16' (default: x's type; bf16 with codes)."""
     return _run(_binding.w4, x, stream, x, weight.packed, weight.n, weight.k, weight.group, weight.scale_dtype, x_scale,
+                _choice(_OUT, out_dtype, "out_dtype"), out)
+
+
+class W8Weight:
+    """A weight matrix [n, k] of 8-bit integers with a scale for each of its n rows (output channels), laid out once
+    for w8_linear.
+
+    codes: int8 [n, k]; scales: fp32 [n]. The packed copy (`packed`, uint8) is all that is kept."""
+
+    def __init__(self, codes, scales, stream=None):
+        _need(codes.dim() == 2 and codes.dtype == torch.int8 and codes.is_contiguous(),
+              "codes must be a contiguous int8 tensor [n, k], got %s %s", codes.dtype, tuple(codes.shape))
+        self.n, self.k = codes.shape
+        _need(scales.dim() == 1 and scales.shape[0] == self.n and scales.is_contiguous()
+              and scales.device == codes.device and scales.dtype == torch.float32,
+              "scales must be a contiguous float32 tensor [%d] on %s", self.n, codes.device)
+        self.device = codes.device
+        need = ctypes.c_size_t()
+        check(lib.rsq_w8_bytes(self.n, self.k, ctypes.byref(need)))
+        with on(codes.get_device(), stream) as s:
+            self.packed = codes.new_empty(need.value, dtype=torch.uint8)
+            check(lib.rsq_w8_pack(codes.data_ptr(), scales.data_ptr(), self.n, self.k, self.packed.data_ptr(), need.value, s))
+        record(stream, codes, scales)
+
+
+def w8_linear(x, weight, x_scale, bias=None, out_dtype=None, out=None, stream=None):
+    """int8 rows x, [rows, k] or [sequences, tokens, k], times a W8Weight [n, k]: y [..., n] (rsq_w8_linear).
+
+    x_scale: fp32, one a row ([...] or [..., 1]), as rms_norm and block_norm return them; bias: fp32 [n]. out_dtype:
+    'bf16' (default) or 'f32'."""
+    return _run(_binding.w8, x, stream, x, weight.packed, weight.n, weight.k, x_scale, bias,
                 _choice(_OUT, out_dtype, "out_dtype"), out)

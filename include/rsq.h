@@ -64,8 +64,8 @@ enum { RSQ_RETNET = 0, RSQ_MAMBA2 = 1, RSQ_GLA = 2, RSQ_GDN = 3 };
 enum { RSQ_SCALE_DYNAMIC = 0, RSQ_SCALE_PERSISTENT = 1, RSQ_SCALE_YOKED = 2 };
 /* Element types. INT8 and E4M3 (OCP, saturating) are 8-bit codes with scales. */
 enum { RSQ_F32 = 0, RSQ_F16 = 1, RSQ_BF16 = 2, RSQ_INT8 = 3, RSQ_E4M3 = 4 };
-/* Activations of rsq_causal_conv. */
-enum { RSQ_ACT_NONE = 0, RSQ_ACT_SILU = 1 };
+/* Activations: of rsq_causal_conv the first two, of rsq_block_norm's gate any. */
+enum { RSQ_ACT_NONE = 0, RSQ_ACT_SILU = 1, RSQ_ACT_SIGMOID = 2 };
 /* rsq_state_alloc modes. */
 enum { RSQ_INIT_ZERO = 0, RSQ_ATTACH = 1 };
 /* Device status bits (rsq_get_status). */
@@ -519,6 +519,44 @@ typedef struct rsq_norm {
 rsq_status rsq_rms_norm(const rsq_norm* norm, void* stream);
 
 /*
+ * Norms before and after a block, with its gate and residual; of each row
+ *   u = x                       (gate_first: x * act(gate))
+ *   u = u / sqrt(mean(u^2) + eps) * weight          (weight NULL: u as it is)
+ *   u = u * act(gate)           (unless it came first; gate NULL: u as it is)
+ *   h = residual + residual_scale * u (stored back to residual, rounded to dtype; NULL: h = u)
+ *   y = h / sqrt(mean(h^2) + eps) * next_weight, of the fp32 h (next_weight NULL: y = h)
+ *   dtype        RSQ_F32 | RSQ_BF16: x, gate, residual
+ *   out_dtype, scale_group, scales  of y, as out_dtype, group and scales of rsq_rms_norm
+ *   group        the first mean's columns: 0 (the row), or a multiple of 8 that
+ *                divides cols (heads normed one by one)
+ *   weight       device fp32 [weight_cols]: cols of them, or one group's for all
+ *   activation   RSQ_ACT_NONE | RSQ_ACT_SILU | RSQ_ACT_SIGMOID
+ *   residual_scale  finite; 1 without a residual
+ *   y            may be NULL where the residual is the result: with a residual,
+ *                without next_weight and codes (out_dtype is then not looked at
+ *                beyond being a type)
+ *   cols         at most 32768
+ * The sums of squares are fp32, as in rsq_rms_norm.
+ */
+typedef struct rsq_block {
+  int32_t dtype, out_dtype, cols, group, weight_cols, scale_group, activation, gate_first;
+  float eps, residual_scale;
+  int64_t rows;
+  const void* x;
+  int64_t x_stride;
+  const void* gate;
+  int64_t gate_stride;
+  void* residual;
+  int64_t residual_stride;
+  const float* weight;
+  const float* next_weight;
+  void* y;
+  int64_t y_stride;
+  float* scales;
+} rsq_block;
+rsq_status rsq_block_norm(const rsq_block* block, void* stream);
+
+/*
  * Products with 4-bit weights: y[m, n] = sum_j x[m, j] codes[n, j] scales[n, j / group].
  *   group        32, 64 or 128, dividing k
  *   codes        device int8 [n][k], values -8..7 (their low four bits are taken)
@@ -550,6 +588,43 @@ typedef struct rsq_w4 {
   int64_t y_stride;
 } rsq_w4;
 rsq_status rsq_w4_linear(const rsq_w4* w4, void* stream);
+
+/*
+ * Products of 8-bit integers with a scale for each token and each channel, for the
+ * projections of prompts:
+ *   y[m, n] = x_scale[m] scales[n] sum_j x[m, j] codes[n, j] (+ bias[n])
+ *   codes        device int8 [n][k], scales device fp32 [n]
+ * rsq_w8_pack lays both out once into `packed` (rsq_w8_bytes bytes, 16-byte
+ * aligned): 16 rows x 64 columns in 1 KB, rows and columns padded with zeros, then
+ * the scales.
+ *   x            device int8 [m][k], rows x_stride bytes apart
+ *   x_scale      device fp32 [m], as rsq_rms_norm and rsq_block_norm give them
+ *   bias         device fp32 [n], or NULL
+ *   out_dtype    RSQ_F32 | RSQ_BF16
+ *   workspace    rsq_w8_workspace bytes, 16-byte aligned (rows of x that do not begin
+ *                at multiples of 16 bytes are laid out again where there are many of
+ *                them; NULL where that is 0). Its contents need not be kept.
+ * Sums are exact (int32: k below 2^17), then rounded to fp32 before the scales. n up
+ * to 2^26 (RSQ_E_UNSUPPORTED beyond).
+ */
+rsq_status rsq_w8_bytes(int32_t n, int32_t k, size_t* bytes);
+rsq_status rsq_w8_pack(const int8_t* codes, const float* scales, int32_t n, int32_t k, void* packed,
+                       size_t packed_bytes, void* stream);
+typedef struct rsq_w8 {
+  int32_t out_dtype, m, n, k;
+  const int8_t* x;
+  int64_t x_stride;
+  const float* x_scale;
+  const float* bias;
+  const void* packed;
+  size_t packed_bytes;
+  void* y;
+  int64_t y_stride;
+  void* workspace;
+  size_t workspace_bytes;
+} rsq_w8;
+rsq_status rsq_w8_workspace(const rsq_w8* w8, size_t* bytes);
+rsq_status rsq_w8_linear(const rsq_w8* w8, void* stream);
 
 /* Thread-local description of the last error (never NULL). */
 const char* rsq_last_error(void);
