@@ -1,5 +1,5 @@
 // Attention with the delta rule over prompts (linear.hpp has the recurrence), in
-// chunks of L tokens. With c_t the sum of log a over a chunk's tokens up to t, S0
+// chunks of kL tokens. With c_t the sum of log a over a chunk's tokens up to t, S0
 // the state before the chunk and n its last token, the chunk's u solve
 //   u_t + sum_{s < t} A_ts u_s = b_t (v_t - e^{c_t} S0^T k_t),  A_ts = b_t e^{c_t - c_s} (k_t . k_s),
 // so that with T = (1 + A)^-1 diag(b), which does not depend on the state,
@@ -17,13 +17,15 @@
 namespace rsq {
 namespace {
 
+constexpr int kL = 64;       // tokens of a chunk
+constexpr int kTiles = kL / 16;
 constexpr int kPieces = 3;   // of fp32 factors that reach the state
+typedef ChunkRows<kL> Rows;
 
 struct DeltaArgs {
   LinearArgs l;
   uint8_t* chunks;    // [slot][head] what a chunk's tokens give (Chunk)
-  uint8_t* keys;      // fp32: [slot][key head][K, Q][pieces] tiles as LDS has them
-  int32_t slots;      // chunks of all sequences, at most
+  uint8_t* keys;      // fp32: [slot][key head][K, Q][pieces][kL][DK] bf16
   int32_t vblocks;    // column blocks of a head
   int32_t units;      // sequences x heads
 };
@@ -31,44 +33,41 @@ struct DeltaArgs {
 // What the first kernel leaves of a chunk and head for the second: fragments of T
 // (pieces of its fp32) and P^T as products of 32 tokens s take them, those with an
 // s <= t only, and the decays.
-template <int L, int PY>
+template <int PY>
 struct Chunk {
-  static constexpr int kTiles = L / 16;                  // of tokens t
-  static constexpr int kFragments = L == 64 ? 6 : 2;
+  static constexpr int kFragments = 6;
   // fragment of tokens t in tile e, s in the j-th 32
   static __device__ constexpr int fragment(int e, int j) { return e < 2 ? e : 2 * e - 2 + j; }
   static constexpr int kT = 0, kP = kFragments * kPieces * 1024, kGates = kP + kFragments * PY * 1024;
   static constexpr int kBytes = kGates + 1024;
-  // floats of the gates: e^{c_t}, e^{c_n - c_t}; then e^{c_n}; the first token whose key or gate is not finite
-  static constexpr int kTo = 0, kFrom = 64, kDecay = 128, kBad = 129;
+  // bytes of the gates: e^{c_t}, e^{c_n - c_t}; then e^{c_n}; the first token whose key or gate is not finite
+  static constexpr int kTo = kGates, kFrom = kTo + 4 * kL, kDecay = kFrom + 4 * kL, kBad = kDecay + 4;
 };
 
-// Chunk j of a sequence that begins at row b is slot b / L + s + j: those of the
+// Chunk j of a sequence that begins at row b is slot b / kL + s + j: those of the
 // sequences before it end below that, whatever their lengths.
-template <int L>
 __device__ __forceinline__ int first_slot(const Sequences& q, int s, int& begin, int& len) {
   int64_t n;
   begin = (int)seq_range(q, s, n);
   len = (int)n;
-  return begin / L + s;
+  return begin / kL + s;
 }
 
 // The sequence of a slot: the last one whose first slot is not above it. 64 sequences
 // are looked at at a time, a 64th of those left apart.
-template <int L>
 __device__ __forceinline__ bool find_chunk(const Sequences& q, int slot, int lane, int& begin, int& len, int& chunk) {
   int lo = 0, n = q.seqs;
   for (;;) {
     const int step = (n + 63) / 64, s = lo + lane * step;
     int b = 0, l = 0;
-    const bool below = lane * step < n && first_slot<L>(q, s, b, l) <= slot;
+    const bool below = lane * step < n && first_slot(q, s, b, l) <= slot;
     const uint64_t hit = __builtin_amdgcn_ballot_w64(below);
     if (!hit) return false;
     const int last = 63 - __builtin_clzll(hit);
     if (step == 1) {
       begin = __builtin_amdgcn_readlane(b, last), len = __builtin_amdgcn_readlane(l, last);
-      chunk = slot - (begin / L + lo + last);
-      return chunk * L < len;
+      chunk = slot - (begin / kL + lo + last);
+      return chunk * kL < len;
     }
     n = min(step, n - last * step);
     lo += last * step;
@@ -81,22 +80,24 @@ __device__ __forceinline__ float exp2_of(double c) { return __builtin_amdgcn_exp
 // inputs' pieces); the inverse in fp32: 16 x 16 blocks on the diagonal by
 // substitution, a column a lane, then the blocks below them, diagonal by diagonal,
 // T_ij = -T_ii sum_k A_ik T_kj, by fp32 products.
-template <typename T, int DK, int L, int PI, int PY>
+template <typename T, int DK, int PI, int PY>
 __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   typedef Tile<DK> TB;
-  typedef Chunk<L, PY> C;
-  constexpr int TT = C::kTiles, KS = DK / 32, LD = L + 4;
-  constexpr int BB = L * TB::kBytes;
-  constexpr int KEYS = 2 * PI * BB, INV = L * LD * 4;
-  // K and Q, and once their products are there, the inverse
+  typedef Chunk<PY> C;
+  constexpr int KS = DK / 32, LD = kL + 4;
+  constexpr int BB = kL * TB::kBytes;
+  constexpr int KEYS = 2 * PI * BB, INV = 2 * kL * LD * 4;
+  // K and Q, and once their products are there, A and its inverse
   __shared__ __attribute__((aligned(16))) uint8_t raw[KEYS > INV ? KEYS : INV];
-  __shared__ __attribute__((aligned(16))) float lds_a[L * LD];
-  __shared__ double lds_c[L];
-  __shared__ __attribute__((aligned(16))) float lds_beta[L];
+  // e^{c_t - c_s} of the chunk's tokens as products: c = n + f in powers of two with n whole,
+  // 2^{f_t} 2^{-f_s} 2^{n_t - n_s}
+  __shared__ __attribute__((aligned(16))) float lds_to[kL], lds_from[kL], lds_beta[kL];
+  __shared__ __attribute__((aligned(16))) int lds_whole[kL];
   __shared__ int lds_bad;
   uint8_t* const lds_k = raw;
   uint8_t* const lds_q = raw + PI * BB;
-  float* const lds_t = reinterpret_cast<float*>(raw);
+  float* const lds_a = reinterpret_cast<float*>(raw);
+  float* const lds_t = lds_a + kL * LD;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -104,20 +105,20 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   const int h = blockIdx.x % a.l.H;
   const int slot = blockIdx.x / a.l.H;
   int begin, len, chunk;
-  if (!find_chunk<L>(a.l.s, slot, lane, begin, len, chunk)) return;
+  if (!find_chunk(a.l.s, slot, lane, begin, len, chunk)) return;
   begin = __builtin_amdgcn_readfirstlane(begin), len = __builtin_amdgcn_readfirstlane(len);
-  const int t0 = __builtin_amdgcn_readfirstlane(chunk) * L;
+  const int t0 = __builtin_amdgcn_readfirstlane(chunk) * kL;
   const int hk = h / a.l.per_key, dk = a.l.dk;
   uint8_t* const blob = a.chunks + ((size_t)slot * a.l.H + h) * C::kBytes;
 
   // ---- rows to LDS
-  constexpr int NB = L * (DK / 8) / 256, RB = 256 / (DK / 8);
+  constexpr int NB = kL * (DK / 8) / 256, RB = 256 / (DK / 8);
   const int row0 = tid / (DK / 8), piece = tid % (DK / 8);
   const int krow = (int)(a.l.k_stride * sizeof(T)), qrow = (int)(a.l.q_stride * sizeof(T));
   Vec8<T, PI> rk[NB], rq[NB];
   {
-    const ChunkRows<L> rK(reinterpret_cast<const T*>(a.l.k) + begin * a.l.k_stride + (size_t)hk * dk, krow, t0, len);
-    const ChunkRows<L> rQ(reinterpret_cast<const T*>(a.l.q) + begin * a.l.q_stride + (size_t)hk * dk, qrow, t0, len);
+    const Rows rK(reinterpret_cast<const T*>(a.l.k) + begin * a.l.k_stride + (size_t)hk * dk, krow, t0, len);
+    const Rows rQ(reinterpret_cast<const T*>(a.l.q) + begin * a.l.q_stride + (size_t)hk * dk, qrow, t0, len);
     const bool in = piece * 8 < dk;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -125,14 +126,14 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
       rq[i].load(rQ, in ? (uint32_t)((row0 + i * RB) * qrow + piece * 8 * (int)sizeof(T)) : kOutside);
     }
   }
-  const bool valid = lane < L && t0 + lane < len;
+  const bool valid = lane < kL && t0 + lane < len;
   float al = 1.f, be = 0.f;
   if (wave == 0 && valid) {
     const int64_t row = (int64_t)begin + t0 + lane;
     if (a.l.alpha) al = a.l.alpha[row * a.l.alpha_stride + h];
     be = a.l.beta[row * a.l.beta_stride + h];
   }
-  if (tid == 0) lds_bad = L;
+  if (tid == 0) lds_bad = kL;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     if (rk[i].bad_bits() & (PI == 1 ? 0x80008000u : 0x80000000u)) atomicMin(&lds_bad, row);
     if constexpr (PI > 1) {
       if (h % a.l.per_key == 0) {
-        uint8_t* const to = a.keys + ((size_t)slot * (a.l.H / a.l.per_key) + hk) * KEYS + at;
+        uint8_t* const to = a.keys + ((size_t)slot * (a.l.H / a.l.per_key) + hk) * KEYS + row * TB::kBytes + piece * 16;
 #pragma unroll
         for (int p = 0; p < PI; ++p) {
           *reinterpret_cast<u32x4*>(to + p * BB) = pk[p];
@@ -163,22 +164,23 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   // NaN: such tokens are left out here, and written as NaN by the second kernel.
   if (wave == 0) {
     const uint64_t odd = __builtin_amdgcn_ballot_w64(valid && !(al >= 0.f && al < __builtin_inff() && fabsf(be) < __builtin_inff()));
-    const int bad = min(lds_bad, odd ? (int)__builtin_ctzll(odd) : L);
+    const int bad = min(lds_bad, odd ? (int)__builtin_ctzll(odd) : kL);
     const bool in = valid && lane < bad;
     double cum = in ? log2((double)al) : 0.;
     cum = cum < -2000. ? -2000. : cum;   // (as good as nothing of an fp32 state is left)
     cum = wave_scan(cum);
     const double last = lane63(cum);
-    float* const gates = reinterpret_cast<float*>(blob + C::kGates);
-    if (lane < L) {
-      lds_c[lane] = cum;
-      lds_beta[lane] = in ? be : 0.f;
-      gates[C::kTo + lane] = exp2_of(cum);
-      gates[C::kFrom + lane] = exp2_of(last - cum);
-    }
+    const double whole = rint(cum);
+    const float f = (float)(cum - whole);
+    lds_to[lane] = __builtin_amdgcn_exp2f(f);
+    lds_from[lane] = __builtin_amdgcn_exp2f(-f);
+    lds_whole[lane] = (int)whole;
+    lds_beta[lane] = in ? be : 0.f;
+    *reinterpret_cast<float*>(blob + C::kTo + 4 * lane) = exp2_of(cum);
+    *reinterpret_cast<float*>(blob + C::kFrom + 4 * lane) = exp2_of(last - cum);
     if (lane == 0) {
-      gates[C::kDecay] = exp2_of(last);
-      reinterpret_cast<int*>(gates)[C::kBad] = bad;
+      *reinterpret_cast<float*>(blob + C::kDecay) = exp2_of(last);
+      *reinterpret_cast<int*>(blob + C::kBad) = bad;
       lds_bad = bad;
     }
   }
@@ -187,20 +189,20 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   // ---- rows s, columns t, of the products with K (for A) and with Q (P^T): two tiles
   // of s at a time, a step of the products that take P
   const uint32_t a_frag = TB::fragment(lane);
-  auto products = [&](int e, bool keys) {
+  auto products = [&](int e, bool keys, f32x4 (&acc)[kL / 32][2]) {
     const uint8_t* const cols = keys ? lds_k : lds_q;
     const int t = 16 * e + n16;
-    const double ct = lds_c[t];
-    const float bt = lds_beta[t];
+    const float to = keys ? lds_to[t] * lds_beta[t] : lds_to[t];
+    const int whole = lds_whole[t];
     u32x4 cf[KS][PI];
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int p = 0; p < PI; ++p) cf[i][p] = *reinterpret_cast<const u32x4*>(cols + p * BB + 16 * e * TB::kBytes + (a_frag ^ (i << 6)));
 #pragma unroll
-    for (int j = 0; j < L / 32; ++j) {
+    for (int j = 0; j < kL / 32; ++j) {
+      acc[j][0] = acc[j][1] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (2 * j > e) continue;
-      f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -210,47 +212,53 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
             const u32x4 kf = *reinterpret_cast<const u32x4*>(lds_k + p * BB + (32 * j + 16 * u) * TB::kBytes + (a_frag ^ (i << 6)));
 #pragma unroll
             for (int q = 0; q < PI; ++q)
-              if (p + q < 3) acc[u] = mfma(kf, cf[i][q], acc[u]);
+              if (p + q < 3) acc[j][u] = mfma(kf, cf[i][q], acc[j][u]);
           }
       settle();
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        const int s0 = 32 * j + 16 * u + 4 * g;
+        const f32x4 from = *reinterpret_cast<const f32x4*>(&lds_from[s0]);
+        const i32x4 n = *reinterpret_cast<const i32x4*>(&lds_whole[s0]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int s = 32 * j + 16 * u + 4 * g + r;
+          const float w = __builtin_amdgcn_ldexpf(acc[j][u][r] * (to * from[r]), whole - n[r]);
           // later tokens, and those from a bad one on, have no part whatever their products are
-          const bool in = s < bad && (keys ? s < t && t < bad : s <= t);
-          const float d = in ? exp2_of(ct - lds_c[s]) : 0.f;
-          acc[u][r] = in ? acc[u][r] * d : 0.f;
-          if (keys) acc[u][r] *= bt;
+          acc[j][u][r] = s0 + r < bad && (keys ? s0 + r < t && t < bad : s0 + r <= t) ? w : 0.f;
         }
-      if (keys) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) *reinterpret_cast<f32x4*>(&lds_a[t * LD + 32 * j + 16 * u + 4 * g]) = acc[u];
-      } else {
-        u32x4 pf[PY];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t lo[PY], hi[PY];
-          split_pair<PY>(acc[u][0], acc[u][1], lo);
-          split_pair<PY>(acc[u][2], acc[u][3], hi);
-#pragma unroll
-          for (int q = 0; q < PY; ++q) pf[q][2 * u] = lo[q], pf[q][2 * u + 1] = hi[q];
-        }
-#pragma unroll
-        for (int q = 0; q < PY; ++q)
-          *reinterpret_cast<u32x4*>(blob + C::kP + ((C::fragment(e, j) * PY + q) * 64 + lane) * 16) = pf[q];
       }
     }
   };
-  if constexpr (L == 64) {
-    products(wave, true);
-    products(3 - wave, false);
-  } else {
-    products(wave & 1, wave < 2);
+  {
+    const int e = 3 - wave;
+    f32x4 p[kL / 32][2];
+    products(e, false, p);
+#pragma unroll
+    for (int j = 0; j < kL / 32; ++j) {
+      if (2 * j > e) continue;
+      u32x4 pf[PY];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t lo[PY], hi[PY];
+        split_pair<PY>(p[j][u][0], p[j][u][1], lo);
+        split_pair<PY>(p[j][u][2], p[j][u][3], hi);
+#pragma unroll
+        for (int q = 0; q < PY; ++q) pf[q][2 * u] = lo[q], pf[q][2 * u + 1] = hi[q];
+      }
+#pragma unroll
+      for (int q = 0; q < PY; ++q)
+        *reinterpret_cast<u32x4*>(blob + C::kP + ((C::fragment(e, j) * PY + q) * 64 + lane) * 16) = pf[q];
+    }
   }
-  __syncthreads();   // K and Q have been read: the inverse takes their place
-  if (wave < TT && lane < 16) {
+  f32x4 kk[kL / 32][2];
+  products(wave, true, kk);
+  __syncthreads();   // K and Q have been read: A and its inverse take their place
+#pragma unroll
+  for (int j = 0; j < kL / 32; ++j)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) *reinterpret_cast<f32x4*>(&lds_a[(16 * wave + n16) * LD + 32 * j + 16 * u + 4 * g]) = kk[j][u];
+  __syncthreads();
+  if (lane < 16) {
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -263,8 +271,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   }
   __syncthreads();
 #pragma unroll
-  for (int d = 1; d < TT; ++d) {
-    if (wave < TT - d) {
+  for (int d = 1; d < kTiles; ++d) {
+    if (wave < kTiles - d) {
       const int j = wave, i = wave + d;
       f32x4 m = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -285,7 +293,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     __syncthreads();
   }
 #pragma unroll
-  for (int e = 0; e < TT; ++e)
+  for (int e = 0; e < kTiles; ++e)
 #pragma unroll
     for (int j = 0; j <= e / 2; ++j) {
       const int f = C::fragment(e, j);
@@ -311,357 +319,494 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     }
 }
 
-// 16 bytes a lane from memory to LDS, at `lds` (uniform over the wavefront) + 16 lane;
-// offsets outside the buffer give zeros. The compiler does not know of these loads:
-// arrived() waits for all of a wavefront's. (m0 is the compiler's for single
-// instructions only, none of which are used here.)
-__device__ __forceinline__ void load_lds(const i32x4& buffer, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(offset), "s"(buffer)
-               : "memory");
-}
-__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-__device__ __forceinline__ i32x4 buffer_of(const void* base, uint32_t bytes) {
+// A buffer at an address that is uniform over the workgroup.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
-  i32x4 r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)p);
-  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32) & 0xFFFF);
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-  r[3] = 0x00020000;
-  return r;
+  const uint32_t low = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+  const uint32_t high = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)high << 32 | low), 0,
+                                           __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)offset, 0, 0);
 }
 
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p);
+// The pieces of a product's factor, 32 of its rows or columns: a lane's first four, then its second four
+typedef u32x2 Halves[2][64];
+__device__ __forceinline__ u32x4 both(const Halves& h, int lane) {
+  const u32x2 lo = h[0][lane], hi = h[1][lane];
+  return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+template <int N>
+__device__ __forceinline__ void put_four(Halves (&h)[N], int half, int lane, const f32x4& v) {
+  uint32_t lo[N], hi[N];
+  split_pair<N>(v[0], v[1], lo);
+  split_pair<N>(v[2], v[3], hi);
+#pragma unroll
+  for (int q = 0; q < N; ++q) h[q][half][lane] = u32x2{lo[q], hi[q]};
 }
 
-// A workgroup owns 16 WV columns of one head's state, a wavefront 16 of them and all
-// of d_k, in registers over the whole sequence. Rows k of the state are spread over
-// the lanes so that a lane's 8 of a step of 32 follow one another, in the order in
-// which a product takes 8 rows of K: state register [kt][r] of lane group g is row
-// 32 (kt / 2) + 8 g + 4 (kt & 1) + r. Results of one product are then factors of the
-// next as they are, S of K S, X of T X, U of P U and K^T U, and nothing but the inputs
-// passes through LDS, which holds two chunks' (one on its way from memory).
-template <typename T, int DK, int L, int PI, int PY, int WV>
-__global__ __launch_bounds__(64 * WV) void delta_kernel(DeltaArgs a) {
-  typedef Tile<DK> TB;
-  typedef Chunk<L, PY> C;
-  constexpr int TT = C::kTiles, KT = DK / 16, KS = DK / 32, TS = L / 32;
-  constexpr int BB = L * TB::kBytes, KEYS = 2 * PI * BB;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][KEYS + C::kBytes];
+// The chain of a sequence's chunks. Eight wavefronts share NC x 16 columns of one head's
+// state. Four of them make U, the four others O and the state, of which each has a
+// quarter of the rows in registers over the whole sequence; U and O each a tile of 16 of
+// a chunk's tokens. A chunk is three steps, with a barrier after each; what a step needs
+// of another wavefront passes through LDS:
+//   1. K S0 and X = V - e^c K S0, from all pieces of S0 | O of the last chunk
+//   2. U = T X, from all pieces of X                    | S0^T Q^T
+//   3. the next chunk's K to LDS                        | S, from all pieces of U and all of K
+// Everything else comes straight from memory into registers, a chunk ahead, each fetch
+// where its wavefront waits for LDS anyway. K passes through LDS to be read as columns,
+// in planes of four of each eight keys, so that such reads take whole runs of banks.
+//
+// Rows k of the state are spread over the lanes so that a lane's 8 of a step of 32
+// follow one another, in the order in which a product takes 8 keys of a token: register
+// r of lane group g in tile kt is row 32 (kt / 2) + 8 g + 4 (kt & 1) + r. Results of one
+// product are then factors of the next as they are.
+template <typename T, int DK, int PI, int PY, int NC>
+__global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
+  typedef Chunk<PY> C;
+  constexpr int KS = DK / 32, KTW = DK / 64;   // steps of 32 keys, a wavefront's tiles of 16 rows
+  constexpr int TS = kL / 32;
+  constexpr int KEYS = 2 * PI * kL * DK * 2;
+  constexpr int CH = NC == 1 ? 3 : 1;   // sums of a product that go side by side
+  __shared__ __attribute__((aligned(16))) Halves lds_s[NC][KS][kPieces], lds_x[NC][TS][kPieces];
+  __shared__ __attribute__((aligned(16))) Halves lds_w[NC][TS][kPieces], lds_u[NC][TS][PY];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][PI][KS][2][kL * 32];
+  __shared__ __attribute__((aligned(16))) u32x2 lds_v[PI == 1 ? 4 : 1][NC][64];
+  __shared__ int lds_first[2][NC * 16];   // first token of a column whose X is not finite
+  __shared__ int lds_any[2];
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+  const bool makes_u = __builtin_amdgcn_readfirstlane(tid >> 8) == 0;
   const int n16 = lane & 15, g = lane >> 4;
   // Workgroups go round the 8 XCDs: those of one head and sequence, which read the
   // same chunks, go to one XCD's cache.
   const int id = blockIdx.x >> 3;
   const int unit = id / a.vblocks * 8 + (blockIdx.x & 7);
   if (unit >= a.units) return;
-  const int v0 = (id % a.vblocks) * 16 * WV;
+  const int v0 = (id % a.vblocks) * 16 * NC;
   const int h = unit % a.l.H, sq = unit / a.l.H, hk = h / a.l.per_key;
   const int dk = a.l.dk, dv = a.l.dv;
   int begin, len;
-  const int slot0 = __builtin_amdgcn_readfirstlane(first_slot<L>(a.l.s, sq, begin, len));
+  const int slot0 = __builtin_amdgcn_readfirstlane(first_slot(a.l.s, sq, begin, len));
   begin = __builtin_amdgcn_readfirstlane(begin), len = __builtin_amdgcn_readfirstlane(len);
-  const int chunks = (len + L - 1) / L;
+  const int chunks = (len + kL - 1) / kL;
   if (chunks == 0 && a.l.state_in) return;
 
-  const int sv = v0 + 16 * wave + n16;
-  float* const st = a.l.state + ((size_t)sq * a.l.H + h) * dk * dv + sv;
-  auto state_row = [&](int kt, int r) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1) + r; };
-  f32x4 S[KT];
+  const int t16 = 16 * wave;   // its tokens
+  auto rows_of = [&](int c) { return max(min(len - c * kL, kL), 0); };   // (none past the last chunk)
+  const size_t blob_step = (size_t)a.l.H * C::kBytes;
+  const uint8_t* blob = a.chunks + ((size_t)slot0 * a.l.H + h) * C::kBytes;
+  auto blob_of = [&](int c) { return buffer(blob, c < chunks ? C::kBytes : 0); };
+  // keys or queries: rows as they are, or the pieces that the first kernel left
+  const int row_bytes = PI == 1 ? (int)((makes_u ? a.l.k_stride : a.l.q_stride) * sizeof(T)) : DK * 2;
+  const uint8_t* key_at = PI == 1 ? reinterpret_cast<const uint8_t*>(makes_u ? a.l.k : a.l.q) + (int64_t)begin * row_bytes + (size_t)hk * dk * 2
+                                  : a.keys + ((size_t)slot0 * (a.l.H / a.l.per_key) + hk) * KEYS + (makes_u ? 0 : KEYS / 2);
+  const size_t key_step = PI == 1 ? (size_t)kL * row_bytes : (size_t)(a.l.H / a.l.per_key) * KEYS;
+  uint32_t key_off[KS];
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt) {
-    S[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (a.l.state_in) {
+  for (int i = 0; i < KS; ++i)
+    key_off[i] = 32 * i + 8 * g < dk ? (uint32_t)((t16 + n16) * row_bytes + 64 * i + 16 * g) : kOutside;
+  u32x4 kf[KS][PI];   // of token n16, eight keys or queries
+  auto fetch_keys = [&](int c) {
+    const auto r = buffer(key_at, PI == 1 ? rows_of(c) * row_bytes : c < chunks ? KEYS / 2 : 0);
+    key_at += key_step;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (state_row(kt, r) < dk && sv < dv) S[kt][r] = st[(size_t)state_row(kt, r) * dv];
-    }
-  }
-
-  const T* const kp = reinterpret_cast<const T*>(a.l.k) + begin * a.l.k_stride + (size_t)hk * dk;
-  const T* const qp = reinterpret_cast<const T*>(a.l.q) + begin * a.l.q_stride + (size_t)hk * dk;
-  const T* const vp = reinterpret_cast<const T*>(a.l.v) + begin * a.l.v_stride + (size_t)h * dv;
-  T* const op = reinterpret_cast<T*>(a.l.o) + begin * a.l.o_stride + (size_t)h * dv;
-  const int krow = (int)(a.l.k_stride * sizeof(T)), qrow = (int)(a.l.q_stride * sizeof(T));
-  const int vrow = (int)(a.l.v_stride * sizeof(T)), orow = (int)(a.l.o_stride * sizeof(T));
-
-  // ---- a chunk's K, Q (fp32: their pieces), T, P and decays to LDS
-  auto fetch = [&](int c) {
-    const uint32_t to = lds_address(lds[c & 1]);
-    if constexpr (PI == 1) {
-      const int rows = min(len - c * L, L);
-      const i32x4 rK = buffer_of(kp + (int64_t)c * L * a.l.k_stride, (uint32_t)(rows * krow));
-      const i32x4 rQ = buffer_of(qp + (int64_t)c * L * a.l.q_stride, (uint32_t)(rows * qrow));
+    for (int i = 0; i < KS; ++i)
 #pragma unroll
-      for (int i0 = 0; i0 < BB / 1024; i0 += WV) {
-        const int i = i0 + wave;
-        if (BB / 1024 % WV != 0 && i >= BB / 1024) break;
-        // LDS holds a row's pieces in Tile's order
-        const int row = (64 * i + lane) / (DK / 8), at = (64 * i + lane) % (DK / 8);
-        const int piece = (int)(TB::at(row, at) - row * TB::kBytes) >> 4;
-        const bool in = piece * 8 < dk;
-        load_lds(rK, in ? (uint32_t)(row * krow + piece * 16) : kOutside, to + i * 1024);
-        load_lds(rQ, in ? (uint32_t)(row * qrow + piece * 16) : kOutside, to + BB + i * 1024);
-      }
-    } else {
-      const i32x4 r = buffer_of(a.keys + ((size_t)(slot0 + c) * (a.l.H / a.l.per_key) + hk) * KEYS, KEYS);
-#pragma unroll
-      for (int i0 = 0; i0 < KEYS / 1024; i0 += WV) {
-        const int i = i0 + wave;
-        if (KEYS / 1024 % WV != 0 && i >= KEYS / 1024) break;
-        load_lds(r, (uint32_t)(i * 1024 + lane * 16), to + i * 1024);
-      }
-    }
-    const i32x4 r = buffer_of(a.chunks + ((size_t)(slot0 + c) * a.l.H + h) * C::kBytes, C::kBytes);
-#pragma unroll
-    for (int i0 = 0; i0 < C::kBytes / 1024; i0 += WV) {
-      const int i = i0 + wave;
-      if (C::kBytes / 1024 % WV != 0 && i >= C::kBytes / 1024) break;
-      load_lds(r, (uint32_t)(i * 1024 + lane * 16), to + KEYS + i * 1024);
-    }
+      for (int p = 0; p < PI; ++p) kf[i][p] = load16(r, key_off[i] + p * kL * DK * 2);
   };
-  uint32_t vn[TT][4];   // v of tokens 16 e + 4 g + r, this lane's column
-  uint32_t voff = sv < dv ? (uint32_t)(4 * g * vrow + sv * (int)sizeof(T)) : kOutside;
-  auto fetch_v = [&](int c) {
-    const ChunkRows<L> rV(vp, vrow, c * L, len);
-#pragma unroll
-    for (int e = 0; e < TT; ++e)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int at = (int)(voff + (uint32_t)((16 * e + r) * vrow));
-        if constexpr (PI == 1) vn[e][r] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rV.rsrc, at, 0, 0) << 16;
-        else vn[e][r] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rV.rsrc, at, 0, 0);
-      }
-  };
-  const uint32_t a_frag = TB::fragment(lane);
-  const uint32_t a_tr = TB::at(4 * g + (n16 >> 2), n16 & 3);
-  const uint32_t ooff = v0 + 16 * wave + 4 * g < dv ? (uint32_t)(n16 * orow + (v0 + 16 * wave + 4 * g) * (int)sizeof(T)) : kOutside;
+  if (tid < 2 * NC * 16) lds_first[tid / (NC * 16)][tid % (NC * 16)] = kL;
+  if (tid < 2) lds_any[tid] = 0;
+  // a lane's place as it names the run of four that it reads columns of: tokens 4 g .. 4 g + 3
+  const int run = (4 * g + (n16 >> 2)) * 32 + (n16 & 3) * 8;
 
-  if (chunks > 0) {
-    fetch(0);
+  if (makes_u) {
+    // ---------------------------------------------------------------- U
+    const uint8_t* v_at = reinterpret_cast<const uint8_t*>(a.l.v) + ((int64_t)begin * a.l.v_stride + (size_t)h * dv) * sizeof(T);
+    const int vrow = (int)(a.l.v_stride * sizeof(T));
+    // v of tokens 4 g + r, this lane's column: bf16 rows are read whole, four columns a lane, and pass through LDS
+    uint32_t voff[NC][PI == 1 ? 1 : 4];
+    u32x2 vrows[NC];
+    uint32_t vn[NC][4];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      if constexpr (PI == 1) {
+        const int col = v0 + 16 * n + 4 * (lane & 3);
+        voff[n][0] = col < dv ? (uint32_t)((t16 + (lane >> 2)) * vrow + col * 2) : kOutside;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          voff[n][r] = v0 + 16 * n + n16 < dv ? (uint32_t)((t16 + 4 * g + r) * vrow + (v0 + 16 * n + n16) * 4) : kOutside;
+      }
+    }
+    auto fetch_v = [&](int c) {
+      const auto rV = buffer(v_at, rows_of(c) * vrow);
+      v_at += (size_t)kL * vrow;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        if constexpr (PI == 1) {
+          vrows[n] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rV, (int)voff[n][0], 0, 0));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) vn[n][r] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rV, (int)voff[n][r], 0, 0);
+        }
+      }
+    };
+    u32x4 tf[TS][kPieces];   // its tile's fragments of T, zeros for tokens s behind them
+    f32x4 to, from;          // decays to tokens 4 g + r, and from them to the chunk's end
+    auto fetch_t = [&](int c) {
+      const auto r = blob_of(c);
+#pragma unroll
+      for (int j = 0; j < TS; ++j)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+          tf[j][p] = load16(r, 2 * j <= wave ? (uint32_t)(C::kT + (C::fragment(wave, j) * kPieces + p) * 1024 + lane * 16) : kOutside);
+      to = __builtin_bit_cast(f32x4, load16(r, C::kTo + 4 * t16 + 16 * g));
+      from = __builtin_bit_cast(f32x4, load16(r, C::kFrom + 4 * t16 + 16 * g));
+    };
+    // K's planes, and v's columns
+    auto put_keys = [&](int c) {
+      uint8_t* const put = &lds_k[c & 1][0][0][0][(t16 + n16) * 32 + g * 8];
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int p = 0; p < PI; ++p) {
+          uint8_t* const at = put + (p * KS + i) * 2 * kL * 32;
+          *reinterpret_cast<u32x2*>(at) = u32x2{kf[i][p][0], kf[i][p][1]};
+          *reinterpret_cast<u32x2*>(at + kL * 32) = u32x2{kf[i][p][2], kf[i][p][3]};
+        }
+      if constexpr (PI == 1) {
+#pragma unroll
+        for (int n = 0; n < NC; ++n) lds_v[wave][n][lane] = vrows[n];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          const u32x2 w = read_tr(reinterpret_cast<const uint8_t*>(lds_v[wave][n]) + run);
+          vn[n][0] = w[0] << 16, vn[n][1] = w[0] & 0xFFFF0000u, vn[n][2] = w[1] << 16, vn[n][3] = w[1] & 0xFFFF0000u;
+        }
+      }
+    };
+
+    fetch_keys(0);
     fetch_v(0);
-  }
-  for (int c = 0; c < chunks; ++c) {
-    arrived();
-    __syncthreads();   // this chunk is in LDS, and the last one has been read
-    if (c + 1 < chunks) fetch(c + 1);
-    const uint8_t* const lds_k = lds[c & 1];
-    const uint8_t* const lds_q = lds_k + PI * BB;
-    const uint8_t* const blob = lds_k + KEYS;
-    const float* const gates = reinterpret_cast<const float*>(blob + C::kGates);
-    local(voff);
-
-    // ---- K S0 (rows t, columns v) and S0^T Q^T (rows v, columns t)
-    f32x4 x[TT], o[TT];
+    fetch_t(0);
+    put_keys(0);
+    __syncthreads();
+    for (int c = 0; c < chunks; ++c) {
+      const int par = c & 1;
+      blob += blob_step;
+      // ---- 1: K S0 (rows t, columns v), X = V - e^c K S0
+      f32x4 x[NC][CH];
 #pragma unroll
-    for (int e = 0; e < TT; ++e) x[e] = o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < NC; ++n)
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      u32x4 sf[kPieces];
+        for (int i = 0; i < CH; ++i) x[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t lo[kPieces], hi[kPieces];
-        split_pair<kPieces>(S[2 * i + u][0], S[2 * i + u][1], lo);
-        split_pair<kPieces>(S[2 * i + u][2], S[2 * i + u][3], hi);
+      for (int i = 0; i < KS; ++i) {
+        u32x4 sf[NC][kPieces];
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) sf[q][2 * u] = lo[q], sf[q][2 * u + 1] = hi[q];
-      }
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
-      for (int p = 0; p < PI; ++p)
+          for (int q = 0; q < kPieces; ++q) sf[n][q] = both(lds_s[n][i][q], lane);
+        // (products that follow one another go to different sums: one waits for the last to its own)
 #pragma unroll
-        for (int e = 0; e < TT; ++e) {
-          const u32x4 kf = *reinterpret_cast<const u32x4*>(lds_k + p * BB + 16 * e * TB::kBytes + (a_frag ^ (i << 6)));
-          const u32x4 qf = *reinterpret_cast<const u32x4*>(lds_q + p * BB + 16 * e * TB::kBytes + (a_frag ^ (i << 6)));
+        for (int p = 0; p < PI; ++p)
 #pragma unroll
           for (int q = 0; q < kPieces; ++q)
-            if (p + q < 3) x[e] = mfma(kf, sf[q], x[e]);
 #pragma unroll
-          for (int q = 0; q < PY; ++q)
-            if (p + q < 3) o[e] = mfma(sf[q], qf, o[e]);
+            for (int n = 0; n < NC; ++n)
+              if (p + q < 3) x[n][(p + 2 * q) % CH] = mfma(kf[i][p], sf[n][q], x[n][(p + 2 * q) % CH]);
+      }
+      float odd = 0.f;   // 0 X, a NaN where X is not finite
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+#pragma unroll
+        for (int i = 1; i < CH; ++i) x[n][0] += x[n][i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[n][0][r] = __builtin_fmaf(-to[r], x[n][0][r], __uint_as_float(vn[n][r]));
+          odd = __builtin_fmaf(0.f, x[n][0][r], odd);
         }
+      }
+      // A product takes all tokens, with weights of zero for later ones: an X that is not
+      // finite is taken out, and its column NaN from its token on
+      if (__builtin_amdgcn_ballot_w64(odd != odd)) {
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if ((__float_as_uint(x[n][0][r]) & 0x7F800000u) == 0x7F800000u) {
+              x[n][0][r] = 0.f;
+              atomicMin(&lds_first[par][16 * n + n16], t16 + 4 * g + r);
+            }
+        lds_any[par] = 1;
+      }
+#pragma unroll
+      for (int n = 0; n < NC; ++n) put_four(lds_x[n][wave >> 1], wave & 1, lane, x[n][0]);
+      __syncthreads();
+      // ---- 2: U = T X
+      f32x4 u[NC][CH];
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < CH; ++i) u[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      u32x4 xf[NC][TS][kPieces];
+#pragma unroll
+      for (int j = 0; j < TS; ++j)
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int q = 0; q < kPieces; ++q) xf[n][j][q] = both(lds_x[n][j][q], lane);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_keys(c + 1);
+      fetch_v(c + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TS; ++j)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+          for (int q = 0; q < kPieces; ++q)
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+              if (p + q < 3) u[n][(p + 2 * q) % CH] = mfma(tf[j][p], xf[n][j][q], u[n][(p + 2 * q) % CH]);
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+#pragma unroll
+        for (int i = 1; i < CH; ++i) u[n][0] += u[n][i];
+        put_four(lds_w[n][wave >> 1], wave & 1, lane, u[n][0] * from);
+        put_four(lds_u[n][wave >> 1], wave & 1, lane, u[n][0]);
+      }
+      __syncthreads();
+      // ---- 3
+      if (tid < NC * 16) lds_first[par ^ 1][tid] = kL;
+      if (tid == NC * 16) lds_any[par ^ 1] = 0;
+      fetch_t(c + 1);
+      put_keys(c + 1);
+      __syncthreads();
     }
-    settle();
-    // ---- X = V - e^c K S0
-    uint32_t odd = 0;
+    return;
+  }
+  // ---------------------------------------------------------------- O and the state
+  float* const st = a.l.state + ((size_t)sq * a.l.H + h) * dk * dv + v0 + n16;
+  auto state_row = [&](int kt, int r) {
+    const int t = wave * KTW + kt;
+    return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r;
+  };
+  f32x4 S[NC][KTW];
 #pragma unroll
-    for (int e = 0; e < TT; ++e) {
-      const f32x4 to = *reinterpret_cast<const f32x4*>(gates + C::kTo + 16 * e + 4 * g);
+  for (int n = 0; n < NC; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[e][r] = __builtin_fmaf(-to[r], x[e][r], __uint_as_float(vn[e][r]));
-        odd |= (__float_as_uint(x[e][r]) & 0x7F800000u) + 0x00800000u;
+    for (int kt = 0; kt < KTW; ++kt) {
+      S[n][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (a.l.state_in) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (state_row(kt, r) < dk && v0 + 16 * n + n16 < dv) S[n][kt][r] = st[(size_t)state_row(kt, r) * dv + 16 * n];
       }
     }
-    if (c + 1 < chunks) fetch_v(c + 1);
-    // A product takes all tokens, with weights of zero for later ones: an X that is not
-    // finite is taken out, and its column NaN from its token on
-    int bad = reinterpret_cast<const int*>(gates)[C::kBad];
-    const bool any = __builtin_amdgcn_ballot_w64((odd & 0x80000000u) != 0 || bad < L) != 0;
-    if (any) {
+  auto put_state = [&]() {
 #pragma unroll
-      for (int e = 0; e < TT; ++e)
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if ((__float_as_uint(x[e][r]) & 0x7F800000u) == 0x7F800000u) bad = min(bad, 16 * e + 4 * g + r);
-      bad = min(bad, __shfl_xor(bad, 16, 64));
-      bad = min(bad, __shfl_xor(bad, 32, 64));
+      for (int kt = 0; kt < KTW; ++kt) put_four(lds_s[n][(wave * KTW + kt) >> 1], (wave * KTW + kt) & 1, lane, S[n][kt]);
+  };
+  uint8_t* o_at = reinterpret_cast<uint8_t*>(a.l.o) + ((int64_t)begin * a.l.o_stride + (size_t)h * dv) * sizeof(T);
+  const int orow = (int)(a.l.o_stride * sizeof(T));
+  uint32_t ooff[NC];
 #pragma unroll
-      for (int e = 0; e < TT; ++e)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * e + 4 * g + r >= bad) x[e][r] = 0.f;
-    }
-    // ---- U = T X
-    u32x4 xf[TS][kPieces];
-#pragma unroll
-    for (int e = 0; e < TT; ++e) {
-      uint32_t lo[kPieces], hi[kPieces];
-      split_pair<kPieces>(x[e][0], x[e][1], lo);
-      split_pair<kPieces>(x[e][2], x[e][3], hi);
-#pragma unroll
-      for (int q = 0; q < kPieces; ++q) xf[e / 2][q][2 * (e & 1)] = lo[q], xf[e / 2][q][2 * (e & 1) + 1] = hi[q];
-    }
-    f32x4 u[TT];
-#pragma unroll
-    for (int e = 0; e < TT; ++e) u[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int n = 0; n < NC; ++n)
+    ooff[n] = v0 + 16 * n + 4 * g < dv ? (uint32_t)((t16 + n16) * orow + (v0 + 16 * n + 4 * g) * (int)sizeof(T)) : kOutside;
+  u32x4 pf[TS][PY];   // its tile's fragments of P^T, zeros for tokens s behind them
+  float to = 0.f;     // decay to token n16
+  float decay = 0.f;  // e^{c_n}
+  int bad = kL;       // the chunk's first token whose key or gates are not finite
+  auto fetch_p = [&](int c) {
+    const auto r = blob_of(c);
 #pragma unroll
     for (int j = 0; j < TS; ++j)
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p)
+      for (int p = 0; p < PY; ++p)
+        pf[j][p] = load16(r, 2 * j <= wave ? (uint32_t)(C::kP + (C::fragment(wave, j) * PY + p) * 1024 + lane * 16) : kOutside);
+    to = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, C::kTo + 4 * t16 + 4 * n16, 0, 0));
+    decay = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, C::kDecay, 0, 0));
+    bad = __builtin_amdgcn_raw_buffer_load_b32(r, C::kBad, 0, 0);
+  };
+  f32x4 o[NC];   // S0^T Q^T
+  // O^T = e^c S0^T Q^T + U^T P^T of a chunk (before the first there are no rows)
+  auto finish = [&](int c) {
+    const int par = c & 1;
+    const int flag = lds_any[par];
+    u32x4 uf[NC][TS][PY];
 #pragma unroll
-        for (int e = 2 * j; e < TT; ++e) {
-          const u32x4 tf = *reinterpret_cast<const u32x4*>(blob + C::kT + ((C::fragment(e, j) * kPieces + p) * 64 + lane) * 16);
-#pragma unroll
-          for (int q = 0; q < kPieces; ++q)
-            if (p + q < 3) u[e] = mfma(tf, xf[j][q], u[e]);
-        }
-    settle();
-    // ---- O^T = e^c S0^T Q^T + U^T P^T
-    {
-      u32x4 uf[TS][PY];
-#pragma unroll
-      for (int e = 0; e < TT; ++e) {
-        uint32_t lo[PY], hi[PY];
-        split_pair<PY>(u[e][0], u[e][1], lo);
-        split_pair<PY>(u[e][2], u[e][3], hi);
-#pragma unroll
-        for (int q = 0; q < PY; ++q) uf[e / 2][q][2 * (e & 1)] = lo[q], uf[e / 2][q][2 * (e & 1) + 1] = hi[q];
-        const float to = gates[C::kTo + 16 * e + n16];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[e][r] *= to;
-      }
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
       for (int j = 0; j < TS; ++j)
 #pragma unroll
-        for (int p = 0; p < PY; ++p)
+        for (int q = 0; q < PY; ++q) uf[n][j][q] = both(lds_u[n][j][q], lane);
 #pragma unroll
-          for (int e = 2 * j; e < TT; ++e) {
-            const u32x4 pf = *reinterpret_cast<const u32x4*>(blob + C::kP + ((C::fragment(e, j) * PY + p) * 64 + lane) * 16);
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int q = 0; q < PY; ++q)
-              if (p + q < PY) o[e] = mfma(uf[j][q], pf, o[e]);
-          }
-    }
-    // ---- S <- e^{c_n} S0 + K^T (e^{c_n - c} U)
-    u32x4 wf[TS][kPieces];
+      for (int r = 0; r < 4; ++r) o[n][r] *= to;
 #pragma unroll
-    for (int e = 0; e < TT; ++e) {
-      const f32x4 from = *reinterpret_cast<const f32x4*>(gates + C::kFrom + 16 * e + 4 * g);
-      uint32_t lo[kPieces], hi[kPieces];
-      split_pair<kPieces>(u[e][0] * from[0], u[e][1] * from[1], lo);
-      split_pair<kPieces>(u[e][2] * from[2], u[e][3] * from[3], hi);
+    for (int j = 0; j < TS; ++j)
 #pragma unroll
-      for (int q = 0; q < kPieces; ++q) wf[e / 2][q][2 * (e & 1)] = lo[q], wf[e / 2][q][2 * (e & 1) + 1] = hi[q];
-    }
-    const float decay = gates[C::kDecay];
+      for (int p = 0; p < PY; ++p)
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
+        for (int q = 0; q < PY; ++q)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[kt][r] *= decay;
-#pragma unroll
-      for (int j = 0; j < TS; ++j)
-#pragma unroll
-        for (int p = 0; p < PI; ++p) {
-          const u32x4 kf = read_tr8<DK>(lds_k + p * BB + 32 * j * TB::kBytes + (a_tr ^ ((kt >> 1) << 6)) + 8 * (kt & 1));
-#pragma unroll
-          for (int q = 0; q < kPieces; ++q)
-            if (p + q < 3) S[kt] = mfma(kf, wf[j][q], S[kt]);
-        }
-    }
+          for (int n = 0; n < NC; ++n)
+            if (p + q < PY) o[n] = mfma(uf[n][j][q], pf[j][p], o[n]);
     settle();
-    if (any) {
-      if (bad < L) {
+    if (__builtin_amdgcn_readfirstlane(flag | (bad < kL)) != 0)
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+      for (int n = 0; n < NC; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[kt][r] = __builtin_nanf("");
-      }
+        for (int r = 0; r < 4; ++r)
+          if (t16 + n16 >= min(bad, lds_first[par][16 * n + 4 * g + r])) o[n][r] = __builtin_nanf("");
+    const auto rO = buffer(o_at, c < 0 ? 0 : rows_of(c) * orow);
+    if (c >= 0) o_at += (size_t)kL * orow;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int from = __shfl(bad, 4 * g + r, 64);
-#pragma unroll
-        for (int e = 0; e < TT; ++e)
-          if (16 * e + n16 >= from) o[e][r] = __builtin_nanf("");
-      }
-    }
-    const ChunkRows<L> rO(op, orow, c * L, len);
-#pragma unroll
-    for (int e = 0; e < TT; ++e) {
-      const int at = (int)(ooff + (uint32_t)(16 * e * orow));
+    for (int n = 0; n < NC; ++n) {
       if constexpr (PI == 1)
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(o[e][0], o[e][1]), bf16_pair(o[e][2], o[e][3])}, rO.rsrc, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(o[n][0], o[n][1]), bf16_pair(o[n][2], o[n][3])}, rO, (int)ooff[n], 0, 0);
       else
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[e]), rO.rsrc, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[n]), rO, (int)ooff[n], 0, 0);
     }
+  };
+#pragma unroll
+  for (int j = 0; j < TS; ++j)
+#pragma unroll
+    for (int p = 0; p < PY; ++p) pf[j][p] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int n = 0; n < NC; ++n) o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  fetch_keys(0);
+  put_state();
+  __syncthreads();
+  for (int c = 0; c < chunks; ++c) {
+    const int par = c & 1;
+    // ---- 1: O of the last chunk
+    finish(c - 1);
+    fetch_p(c);
+    blob += blob_step;
+    __syncthreads();
+    // ---- 2: S0^T Q^T (rows v, columns t)
+#pragma unroll
+    for (int n = 0; n < NC; ++n) o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      u32x4 sf[NC][PY];
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int q = 0; q < PY; ++q) sf[n][q] = both(lds_s[n][i][q], lane);
+#pragma unroll
+      for (int p = 0; p < PI; ++p)
+#pragma unroll
+        for (int q = 0; q < PY; ++q)
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+            if (p + q < 3) o[n] = mfma(sf[n][q], kf[i][p], o[n]);
+    }
+    settle();
+    __syncthreads();
+    // ---- 3: S <- e^{c_n} S0 + K^T (e^{c_n - c} U)
+    const int flag = lds_any[par];
+    const uint8_t* const k_get = &lds_k[par][0][0][0][run];
+    f32x4 add[NC][KTW];
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int kt = 0; kt < KTW; ++kt) add[n][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < TS; ++j) {
+      u32x4 wf[NC][kPieces];
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) wf[n][q] = both(lds_w[n][j][q], lane);
+#pragma unroll
+      for (int p = 0; p < PI; ++p) {
+        u32x4 kc[KTW];
+#pragma unroll
+        for (int kt = 0; kt < KTW; ++kt) {
+          const int t = wave * KTW + kt;
+          const uint8_t* const at = k_get + ((p * KS + (t >> 1)) * 2 + (t & 1)) * kL * 32 + 32 * j * 32;
+          const u32x2 lo = read_tr(at), hi = read_tr(at + 16 * 32);
+          kc[kt] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q)
+#pragma unroll
+          for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+              if (p + q < 3) add[n][kt] = mfma(kc[kt], wf[n][q], add[n][kt]);
+      }
+      if (j == 0) fetch_keys(c + 1);
+    }
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[n][kt][r] = __builtin_fmaf(S[n][kt][r], decay, add[n][kt][r]);
+    if (__builtin_amdgcn_readfirstlane(flag | (bad < kL)) != 0)
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        if (min(bad, lds_first[par][16 * n + n16]) < kL)
+#pragma unroll
+          for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[n][kt][r] = __builtin_nanf("");
+    put_state();
+    __syncthreads();
   }
+  if (chunks > 0) finish(chunks - 1);
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
+  for (int n = 0; n < NC; ++n)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (state_row(kt, r) < dk && sv < dv) st[(size_t)state_row(kt, r) * dv] = S[kt][r];
+    for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (state_row(kt, r) < dk && v0 + 16 * n + n16 < dv) st[(size_t)state_row(kt, r) * dv + 16 * n] = S[n][kt][r];
 }
 
 typedef void (*DeltaFn)(DeltaArgs);
 
 struct DeltaPlan {
-  int L, waves;
   DeltaFn prepare, scan;
   int64_t slots, units, vblocks;
   size_t chunk_bytes, bytes;
 };
 
-template <typename T, int DK, int L, int PI, int PY>
+template <typename T, int DK, int PI, int PY>
 void pick_delta(DeltaPlan& w, const rsq_linear_attn* p) {
-  w.L = L;
-  w.prepare = delta_prepare_kernel<T, DK, L, PI, PY>;
-  const int64_t tiles = ceil_div(p->d_v, 16);
+  w.prepare = delta_prepare_kernel<T, DK, PI, PY>;
   w.units = (int64_t)p->seqs * p->heads;
-  w.waves = tiles > 4 && w.units >= 128 ? 8 : tiles > 2 && w.units * ceil_div(tiles, 4) >= 64 ? 4 : 1;
-  w.scan = w.waves == 8 ? delta_kernel<T, DK, L, PI, PY, 8> : w.waves == 4 ? delta_kernel<T, DK, L, PI, PY, 4>
-                                                                           : delta_kernel<T, DK, L, PI, PY, 1>;
-  w.vblocks = ceil_div(tiles, w.waves);
-  // a sequence of len rows has ceil(len / L) chunks; with their rows apart, at most tokens / L + seqs in all
-  w.slots = p->tokens / L + p->seqs;
-  w.chunk_bytes = (size_t)w.slots * p->heads * Chunk<L, PY>::kBytes;
-  w.bytes = w.chunk_bytes + (PI > 1 ? (size_t)w.slots * p->key_heads * 2 * PI * L * DK * 2 : 0);
+  const int64_t tiles = ceil_div(p->d_v, 16);
+  constexpr int kMost = PI > 1 || DK > 128 ? 2 : 4;   // (four take more LDS or registers than there are)
+  const int nc = w.units * tiles <= 512 ? 1 : w.units * ceil_div(tiles, 2) <= 1024 ? 2 : kMost;
+  w.scan = nc == 1 ? delta_kernel<T, DK, PI, PY, 1> : nc == 2 ? delta_kernel<T, DK, PI, PY, 2> : delta_kernel<T, DK, PI, PY, kMost>;
+  w.vblocks = ceil_div(tiles, nc);
+  // a sequence of len rows has ceil(len / kL) chunks; with their rows apart, at most tokens / kL + seqs in all
+  w.slots = p->tokens / kL + p->seqs;
+  w.chunk_bytes = (size_t)w.slots * p->heads * Chunk<PY>::kBytes;
+  w.bytes = w.chunk_bytes + (PI > 1 ? (size_t)w.slots * p->key_heads * 2 * PI * kL * DK * 2 : 0);
 }
 
 rsq_status plan_delta(const rsq_linear_attn* p, DeltaPlan& w) {
   if (p->dtype == RSQ_BF16) {
-    if (p->d_k <= 64) pick_delta<Bf16, 64, 64, 1, 2>(w, p);
-    else if (p->d_k <= 128) pick_delta<Bf16, 128, 64, 1, 2>(w, p);
-    else pick_delta<Bf16, 256, 32, 1, 2>(w, p);
+    if (p->d_k <= 64) pick_delta<Bf16, 64, 1, 2>(w, p);
+    else if (p->d_k <= 128) pick_delta<Bf16, 128, 1, 2>(w, p);
+    else pick_delta<Bf16, 256, 1, 2>(w, p);
   } else {
-    if (p->d_k <= 64) pick_delta<float, 64, 32, 3, 3>(w, p);
-    else pick_delta<float, 128, 32, 3, 3>(w, p);
+    if (p->d_k <= 64) pick_delta<float, 64, 3, 3>(w, p);
+    else pick_delta<float, 128, 3, 3>(w, p);
   }
   if (const rsq_status s = check_blocks(w.slots * p->heads, 256)) return s;
-  return check_blocks(ceil_div(w.units, 8) * 8 * w.vblocks, 64 * w.waves);
+  return check_blocks(ceil_div(w.units, 8) * 8 * w.vblocks, 512);
 }
 
 }  // namespace
@@ -685,13 +830,13 @@ rsq_status run_delta(const rsq_linear_attn* p, const LinearArgs& l, void* stream
   a.l = l;
   a.chunks = static_cast<uint8_t*>(p->workspace);
   a.keys = a.chunks + w.chunk_bytes;
-  a.slots = (int32_t)w.slots, a.vblocks = (int32_t)w.vblocks, a.units = (int32_t)w.units;
+  a.vblocks = (int32_t)w.vblocks, a.units = (int32_t)w.units;
   if (p->max_len > 0) {
     hipLaunchKernelGGL(w.prepare, dim3((unsigned)(w.slots * p->heads)), dim3(256), 0, (hipStream_t)stream, a);
     if (const rsq_status s = launched("delta rule, chunks")) return s;
   }
   const int64_t blocks = ceil_div(w.units, 8) * 8 * w.vblocks;
-  hipLaunchKernelGGL(w.scan, dim3((unsigned)blocks), dim3(64 * w.waves), 0, (hipStream_t)stream, a);
+  hipLaunchKernelGGL(w.scan, dim3((unsigned)blocks), dim3(512), 0, (hipStream_t)stream, a);
   return launched("delta rule");
 }
 
