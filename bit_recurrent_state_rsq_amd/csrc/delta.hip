@@ -30,15 +30,15 @@ struct DeltaArgs {
   int32_t units;      // sequences x heads
 };
 
-// What the first kernel leaves of a chunk and head for the second: fragments of T
-// (pieces of its fp32) and P^T as products of 32 tokens s take them, those with an
-// s <= t only, and the decays.
+// What the first kernel leaves of a chunk and head for the second: fragments of T (fp32,
+// to be split where there is time) and P^T (pieces) as products of 32 tokens s take
+// them, those with an s <= t only, and the decays.
 template <int PY>
 struct Chunk {
   static constexpr int kFragments = 6;
   // fragment of tokens t in tile e, s in the j-th 32
   static __device__ constexpr int fragment(int e, int j) { return e < 2 ? e : 2 * e - 2 + j; }
-  static constexpr int kT = 0, kP = kFragments * kPieces * 1024, kGates = kP + kFragments * PY * 1024;
+  static constexpr int kT = 0, kP = kFragments * 2048, kGates = kP + kFragments * PY * 1024;
   static constexpr int kBytes = kGates + 1024;
   // bytes of the gates: e^{c_t}, e^{c_n - c_t}; then e^{c_n}; the first token whose key or gate is not finite
   static constexpr int kTo = kGates, kFrom = kTo + 4 * kL, kDecay = kFrom + 4 * kL, kBad = kDecay + 4;
@@ -299,23 +299,16 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
       const int f = C::fragment(e, j);
       if (f % 4 != wave) continue;
       const int t = 16 * e + n16;
-      u32x4 tf[kPieces];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int s = 32 * j + 16 * u + 4 * g;
         const f32x4 v = *reinterpret_cast<const f32x4*>(&lds_t[t * LD + s]);
         const f32x4 b = *reinterpret_cast<const f32x4*>(&lds_beta[s]);
-        float w[4];
+        f32x4 w;
 #pragma unroll
         for (int r = 0; r < 4; ++r) w[r] = s + r <= t ? v[r] * b[r] : 0.f;   // (above the diagonal nothing is written)
-        uint32_t lo[kPieces], hi[kPieces];
-        split_pair<kPieces>(w[0], w[1], lo);
-        split_pair<kPieces>(w[2], w[3], hi);
-#pragma unroll
-        for (int q = 0; q < kPieces; ++q) tf[q][2 * u] = lo[q], tf[q][2 * u + 1] = hi[q];
+        *reinterpret_cast<f32x4*>(blob + C::kT + ((f * 2 + u) * 64 + lane) * 16) = w;
       }
-#pragma unroll
-      for (int q = 0; q < kPieces; ++q) *reinterpret_cast<u32x4*>(blob + C::kT + ((f * kPieces + q) * 64 + lane) * 16) = tf[q];
     }
 }
 
@@ -329,6 +322,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int b
 }
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)offset, 0, 0);
+}
+
+// The sequence that is the i-th longest, of up to 64: workgroups start in their order, and
+// the long chains must not be the last (8 prompts of 8192 tokens by random cuts, 32 heads
+// of 128 x 128 bf16, IN_ORDER us by length, AS_GIVEN as given).
+__device__ __forceinline__ int longest(const Sequences& q, int i, int lane) {
+  if (!q.offsets || q.seqs > 64 || q.seqs == 1) return i;
+  int b, l = -1;
+  if (lane < q.seqs) first_slot(q, lane, b, l);
+  int rank = 0;
+  for (int j = 0; j < q.seqs; ++j) {
+    const int other = __builtin_amdgcn_readlane(l, j);
+    rank += other > l || (other == l && j < lane) ? 1 : 0;
+  }
+  return (int)__builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < q.seqs && rank == i));
 }
 
 // The pieces of a product's factor, 32 of its rows or columns: a lane's first four, then its second four
@@ -386,7 +394,8 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
   const int unit = id / a.vblocks * 8 + (blockIdx.x & 7);
   if (unit >= a.units) return;
   const int v0 = (id % a.vblocks) * 16 * NC;
-  const int h = unit % a.l.H, sq = unit / a.l.H, hk = h / a.l.per_key;
+  const int h = unit % a.l.H, hk = h / a.l.per_key;
+  const int sq = __builtin_amdgcn_readfirstlane(longest(a.l.s, unit / a.l.H, lane));
   const int dk = a.l.dk, dv = a.l.dv;
   int begin, len;
   const int slot0 = __builtin_amdgcn_readfirstlane(first_slot(a.l.s, sq, begin, len));
@@ -454,17 +463,34 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
         }
       }
     };
-    u32x4 tf[TS][kPieces];   // its tile's fragments of T, zeros for tokens s behind them
+    // its tile's fragments of T, zeros for tokens s behind them; the next chunk's as loaded
+    u32x4 tf[TS][kPieces], tn[TS][2];
     f32x4 to, from;          // decays to tokens 4 g + r, and from them to the chunk's end
     auto fetch_t = [&](int c) {
       const auto r = blob_of(c);
 #pragma unroll
       for (int j = 0; j < TS; ++j)
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p)
-          tf[j][p] = load16(r, 2 * j <= wave ? (uint32_t)(C::kT + (C::fragment(wave, j) * kPieces + p) * 1024 + lane * 16) : kOutside);
+        for (int u = 0; u < 2; ++u)
+          tn[j][u] = load16(r, 2 * j <= wave ? (uint32_t)(C::kT + (C::fragment(wave, j) * 2 + u) * 1024 + lane * 16) : kOutside);
+    };
+    auto fetch_decays = [&](int c) {
+      const auto r = blob_of(c);
       to = __builtin_bit_cast(f32x4, load16(r, C::kTo + 4 * t16 + 16 * g));
       from = __builtin_bit_cast(f32x4, load16(r, C::kFrom + 4 * t16 + 16 * g));
+    };
+    auto split_t = [&]() {
+#pragma unroll
+      for (int j = 0; j < TS; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const f32x4 v = __builtin_bit_cast(f32x4, tn[j][u]);
+          uint32_t lo[kPieces], hi[kPieces];
+          split_pair<kPieces>(v[0], v[1], lo);
+          split_pair<kPieces>(v[2], v[3], hi);
+#pragma unroll
+          for (int q = 0; q < kPieces; ++q) tf[j][q][2 * u] = lo[q], tf[j][q][2 * u + 1] = hi[q];
+        }
     };
     // K's planes, and v's columns
     auto put_keys = [&](int c) {
@@ -488,14 +514,17 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
       }
     };
 
+    fetch_t(0);
+    fetch_decays(0);
     fetch_keys(0);
     fetch_v(0);
-    fetch_t(0);
+    split_t();
+    blob += blob_step;
+    fetch_t(1);
     put_keys(0);
     __syncthreads();
     for (int c = 0; c < chunks; ++c) {
       const int par = c & 1;
-      blob += blob_step;
       // ---- 1: K S0 (rows t, columns v), X = V - e^c K S0
       f32x4 x[NC][CH];
 #pragma unroll
@@ -582,7 +611,10 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
       // ---- 3
       if (tid < NC * 16) lds_first[par ^ 1][tid] = kL;
       if (tid == NC * 16) lds_any[par ^ 1] = 0;
-      fetch_t(c + 1);
+      fetch_decays(c + 1);
+      split_t();
+      blob += blob_step;
+      fetch_t(c + 2);
       put_keys(c + 1);
       __syncthreads();
     }
@@ -787,7 +819,7 @@ void pick_delta(DeltaPlan& w, const rsq_linear_attn* p) {
   w.units = (int64_t)p->seqs * p->heads;
   const int64_t tiles = ceil_div(p->d_v, 16);
   constexpr int kMost = PI > 1 || DK > 128 ? 2 : 4;   // (four take more LDS or registers than there are)
-  const int nc = w.units * tiles <= 512 ? 1 : w.units * ceil_div(tiles, 2) <= 1024 ? 2 : kMost;
+  const int nc = w.units * ceil_div(tiles, 4) >= 256 ? kMost : w.units * tiles > 320 ? 2 : 1;
   w.scan = nc == 1 ? delta_kernel<T, DK, PI, PY, 1> : nc == 2 ? delta_kernel<T, DK, PI, PY, 2> : delta_kernel<T, DK, PI, PY, kMost>;
   w.vblocks = ceil_div(tiles, nc);
   // a sequence of len rows has ceil(len / kL) chunks; with their rows apart, at most tokens / kL + seqs in all
