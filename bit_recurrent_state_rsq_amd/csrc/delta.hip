@@ -325,8 +325,8 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t offse
 }
 
 // The sequence that is the i-th longest, of up to 64: workgroups start in their order, and
-// the long chains must not be the last (8 prompts of 8192 tokens by random cuts, 32 heads
-// of 128 x 128 bf16, IN_ORDER us by length, AS_GIVEN as given).
+// the long chains must not be the last (8192 tokens cut into eight prompts at random, 32
+// heads of 128 x 128 bf16: 277 us by length, 309 as given).
 __device__ __forceinline__ int longest(const Sequences& q, int i, int lane) {
   if (!q.offsets || q.seqs > 64 || q.seqs == 1) return i;
   int b, l = -1;
@@ -813,17 +813,31 @@ struct DeltaPlan {
   size_t chunk_bytes, bytes;
 };
 
+// Column tiles of a workgroup. More of them share a chunk's reading, fewer leave a shorter
+// chain. A chunk takes a workgroup of one, two and four tiles 1.6, 2.45 and 4.2 us, and a
+// compute unit that has others to go on with 1.83, 1.33 and 1.31 us a tile (128 x 128
+// bf16): the longest sequence takes its chunks one after another, and all that the
+// 256 compute units share. By the longer of the two, us, the first tiles chosen: 8192 tokens
+// of 32 heads one 304, two 392, four 621; of 64 heads two 499, one 578, four 687; of 128 four
+// 871, two 948, one 1067.
 template <typename T, int DK, int PI, int PY>
 void pick_delta(DeltaPlan& w, const rsq_linear_attn* p) {
   w.prepare = delta_prepare_kernel<T, DK, PI, PY>;
   w.units = (int64_t)p->seqs * p->heads;
   const int64_t tiles = ceil_div(p->d_v, 16);
-  constexpr int kMost = PI > 1 || DK > 128 ? 2 : 4;   // (four take more LDS or registers than there are)
-  const int nc = w.units * ceil_div(tiles, 4) >= 256 ? kMost : w.units * tiles > 320 ? 2 : 1;
-  w.scan = nc == 1 ? delta_kernel<T, DK, PI, PY, 1> : nc == 2 ? delta_kernel<T, DK, PI, PY, 2> : delta_kernel<T, DK, PI, PY, kMost>;
-  w.vblocks = ceil_div(tiles, nc);
   // a sequence of len rows has ceil(len / kL) chunks; with their rows apart, at most tokens / kL + seqs in all
   w.slots = p->tokens / kL + p->seqs;
+  constexpr int kMost = PI > 1 || DK > 128 ? 2 : 4;   // (four take more LDS or registers than there are)
+  constexpr float kChain[3] = {1.6f, 2.45f, 4.2f}, kTile[3] = {1.83f, 1.33f, 1.31f};
+  float best = 0.f;
+  int nc = 0;
+  for (int i = 0; 1 << i <= kMost; ++i) {
+    const float shared = (float)(w.slots * p->heads) * (float)(ceil_div(tiles, 1 << i) << i) * kTile[i] / 256.f;
+    const float chain = (float)ceil_div(p->max_len, kL) * kChain[i], time = chain > shared ? chain : shared;
+    if (nc == 0 || time < best) best = time, nc = 1 << i;
+  }
+  w.scan = nc == 1 ? delta_kernel<T, DK, PI, PY, 1> : nc == 2 ? delta_kernel<T, DK, PI, PY, 2> : delta_kernel<T, DK, PI, PY, kMost>;
+  w.vblocks = ceil_div(tiles, nc);
   w.chunk_bytes = (size_t)w.slots * p->heads * Chunk<PY>::kBytes;
   w.bytes = w.chunk_bytes + (PI > 1 ? (size_t)w.slots * p->key_heads * 2 * PI * kL * DK * 2 : 0);
 }

@@ -312,15 +312,14 @@ struct W8Pick {
 };
 
 W8Pick pick_w8(int64_t m, int tiles) {
-  const int64_t mtiles = ceil_div(m, 16);
-  if (mtiles <= 2) {
-    if (mtiles == 2) return {w8_few_kernel<4, 2, 4>, 32, 4, 4, false};
-    if (tiles < 384) return {w8_few_kernel<1, 1, 16>, 16, 1, 16, false};
-    return {w8_few_kernel<2, 1, 8>, 16, 2, 8, false};
-  }
-  if (ceil_div(m, 256) * ceil_div(tiles, 16) >= 128) return {w8_kernel<256, 256, 2, 4, 4>, 256, 16, 8, true};
-  if (ceil_div(m, 128) * ceil_div(tiles, 8) >= 128) return {w8_kernel<128, 128, 2, 2, 4>, 128, 8, 4, true};
-  return {w8_kernel<64, 64, 2, 2, 4>, 64, 4, 4, true};
+  const int64_t mtiles = ceil_div(m, 16), work = mtiles * tiles;
+  if (work <= 600) return {w8_few_kernel<2, 1, 16>, 16, 2, 16, false};
+  if (mtiles == 1 || work <= 1300) return {w8_few_kernel<4, 1, 8>, 16, 4, 8, false};
+  if (work <= 2600) return {w8_few_kernel<4, 2, 4>, 32, 4, 4, false};
+  const int64_t large = ceil_div(m, 256) * ceil_div(tiles, 16), rounds = ceil_div(large, 256);
+  if (large >= 160 && (rounds == 1 || large * 5 >= rounds * 256 * 4)) return {w8_kernel<256, 256, 2, 4, 4>, 256, 16, 8, true};
+  if (work <= 9000) return {w8_kernel<64, 64, 2, 2, 4>, 64, 4, 4, true};
+  return {w8_kernel<64, 128, 2, 2, 4>, 64, 8, 4, true};
 }
 
 constexpr int64_t kMaxStride = 1 << 22;   // 256 rows then end below 2^30
