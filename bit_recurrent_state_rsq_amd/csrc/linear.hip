@@ -98,20 +98,21 @@ rsq_ssm as_scan(const rsq_linear_attn* p) {
 // operations an element: bound by memory. With u the token's value,
 //   o = a S^T q + (k . q) u,   u = b (v - a S^T k),
 // so both sums over the rows come from one reading of the state, which stays in
-// registers until u is known. A workgroup owns 64 columns of a head's state; a thread
+// registers until u is known. A workgroup owns 64 or 128 columns of a head's state; a thread
 // owns four consecutive columns and every 16th row. The sums meet in a fixed order.
-constexpr int kColumns = 64, kRows = 16;   // columns of a workgroup, rows at once
+constexpr int kRows = 16;   // rows at once
 
-template <typename T, int NR>
-__global__ __launch_bounds__(256) void linear_step_kernel(LinearArgs a, int32_t vblocks) {
-  __shared__ float part[4][2][kColumns], part_qk[4];
+template <typename T, int NR, int COLS>   // columns of a workgroup: 64 or 128
+__global__ __launch_bounds__(COLS / 4 * kRows) void linear_step_kernel(LinearArgs a, int32_t vblocks) {
+  constexpr int FOURS = COLS / 4, WAVES = FOURS * kRows / 64;
+  __shared__ float part[WAVES][2][COLS], part_qk[WAVES];
   const int64_t id = blockIdx.x / vblocks;
   const int vb = blockIdx.x % vblocks;
   const int h = (int)(id % a.H);
   const int64_t s = id / a.H;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = threadIdx.x % (kColumns / 4), r0 = threadIdx.x / (kColumns / 4);
-  const int col = vb * kColumns + 4 * c;
+  const int c = threadIdx.x % FOURS, r0 = threadIdx.x / FOURS;
+  const int col = vb * COLS + 4 * c;
   const bool in = col < a.dv;   // (d_v is a multiple of 4)
   const T* q = reinterpret_cast<const T*>(a.q) + s * a.q_stride + (int64_t)(h / a.per_key) * a.dk;
   const T* k = reinterpret_cast<const T*>(a.k) + s * a.k_stride + (int64_t)(h / a.per_key) * a.dk;
@@ -146,23 +147,27 @@ __global__ __launch_bounds__(256) void linear_step_kernel(LinearArgs a, int32_t 
     qk = __builtin_fmaf(kf[i], qf[i], qk);
   }
 #pragma unroll
-  for (int x = 16; x <= 32; x <<= 1) {
+  for (int x = FOURS; x <= 32; x <<= 1) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) ks[e] += __shfl_xor(ks[e], x, 64), qs[e] += __shfl_xor(qs[e], x, 64);
     qk += __shfl_xor(qk, x, 64);
   }
-  if (lane < 16) {
+  if (lane < FOURS) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[wave][0][4 * c + e] = ks[e], part[wave][1][4 * c + e] = qs[e];
     if (lane == 0) part_qk[wave] = qk;
   }
   __syncthreads();
-  qk = part_qk[0] + part_qk[1] + part_qk[2] + part_qk[3];
+  qk = part_qk[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) qk += part_qk[w];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int j = 4 * c + e;
-    if (a.beta) u[e] = beta * (u[e] - (part[0][0][j] + part[1][0][j] + part[2][0][j] + part[3][0][j]));
-    qs[e] = part[0][1][j] + part[1][1][j] + part[2][1][j] + part[3][1][j];
+    ks[e] = part[0][0][j], qs[e] = part[0][1][j];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) ks[e] += part[w][0][j], qs[e] += part[w][1][j];
+    if (a.beta) u[e] = beta * (u[e] - ks[e]);
   }
   if (!in) return;
 #pragma unroll
@@ -183,9 +188,9 @@ __global__ __launch_bounds__(256) void linear_step_kernel(LinearArgs a, int32_t 
 }
 
 typedef void (*LinearStepFn)(LinearArgs, int32_t);
-template <typename T>
+template <typename T, int COLS>
 LinearStepFn pick_step(int dk) {
-  return dk <= 64 ? linear_step_kernel<T, 4> : dk <= 128 ? linear_step_kernel<T, 8> : linear_step_kernel<T, 16>;
+  return dk <= 64 ? linear_step_kernel<T, 4, COLS> : dk <= 128 ? linear_step_kernel<T, 8, COLS> : linear_step_kernel<T, 16, COLS>;
 }
 
 }  // namespace
@@ -212,10 +217,15 @@ extern "C" rsq_status rsq_linear_attention(const rsq_linear_attn* p, void* strea
 extern "C" rsq_status rsq_linear_attention_step(const rsq_linear_attn* p, void* stream) {
   if (const rsq_status s = check_linear(p, false)) return s;
   if (const rsq_status s = check_linear_memory(p)) return s;
-  const int64_t vblocks = ceil_div(p->d_v, kColumns);
+  // 128 columns where there are workgroups for four on each of 256 compute units: 64 tokens of 32
+  // heads of 128 x 128 61 us (64 columns 63), one token 6.2 (5.2).
+  const int cols = p->d_v <= 64 || (int64_t)p->seqs * p->heads * ceil_div(p->d_v, 128) < 1024 ? 64 : 128;
+  const int threads = cols / 4 * kRows;
+  const int64_t vblocks = ceil_div(p->d_v, cols);
   const int64_t blocks = (int64_t)p->seqs * p->heads * vblocks;
-  if (const rsq_status s = check_blocks(blocks, 256)) return s;
-  const LinearStepFn fn = p->dtype == RSQ_BF16 ? pick_step<Bf16>(p->d_k) : pick_step<float>(p->d_k);
-  hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, linear_args(p), (int32_t)vblocks);
+  if (const rsq_status s = check_blocks(blocks, threads)) return s;
+  const LinearStepFn fn = p->dtype == RSQ_BF16 ? (cols == 64 ? pick_step<Bf16, 64>(p->d_k) : pick_step<Bf16, 128>(p->d_k))
+                                               : (cols == 64 ? pick_step<float, 64>(p->d_k) : pick_step<float, 128>(p->d_k));
+  hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(threads), 0, (hipStream_t)stream, linear_args(p), (int32_t)vblocks);
   return launched("linear attention step");
 }
