@@ -300,10 +300,11 @@ def test_w8_captured_and_replayed():
 def test_w8_on_another_stream():
     x, codes, scales, xs, bias = w8_case(500, 1000, 300)
     want = rsq.w8_linear(x, rsq.W8Weight(codes, scales), xs, bias=bias)
+    xb = x.to(BF16)
     side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
+    side.wait_stream(torch.cuda.current_stream())   # for all that the operands' own stream does to them
     w = rsq.W8Weight(codes, scales, stream=side)
     y = rsq.w8_linear(x, w, xs, bias=bias, stream=side)
-    z = rsq.block_norm(x.to(BF16), stream=side, out_dtype="f32")
+    z = rsq.block_norm(xb, stream=side, out_dtype="f32")
     side.synchronize()
     assert torch.equal(y, want) and torch.equal(z, x.float())
