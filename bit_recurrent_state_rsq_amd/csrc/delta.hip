@@ -8,6 +8,21 @@
 //   S <- e^{c_n} S0 + K^T (e^{c_n - c} U).
 // delta_prepare_kernel makes T and P of all chunks side by side; delta_kernel then
 // follows the state through a sequence's chunks.
+//
+// 16384 tokens of 32 heads of 128 x 128 with 16 key heads (bf16, 411 MB, 60 GFLOP of the
+// recurrence's own operations: 80 us) take 511 us: 99 for the chunks, which is memory (32 KB
+// read, 25 written a chunk and head, 4.7 TB/s), and 410 for the chain of 256 chunks. A chunk of it
+// takes 1.6 us, three steps of about 1100 cycles: in the first the state's pieces come
+// through LDS (64 KB for eight wavefronts), in the second the products with T, in the third
+// the state's update and its splitting into pieces, each step with an LDS round trip and a
+// barrier; the products themselves are 800 cycles of a SIMD. A compute unit alone takes no
+// less with fewer loads than 1.3 us; with all 256 busy, the 57 KB a chunk that each workgroup
+// reads from its XCD's cache are the other limit. Measured without gain: K and Q copied
+// into whole rows by the first kernel, the next chunk but one called into the cache ahead,
+// raised priority for the wavefronts that make U, T's pieces stored as such (511 -> 566:
+// more to read), a wavefront for 16 columns and all rows (no exchange, but 182 products and
+// 800 vector instructions one after another: 1.1 ms), parts of K S0 summed through LDS (744 us).
+// States keep 1.3e-7 of their norm; two pieces instead of three would leave 2.4e-6.
 #include <algorithm>
 
 #include "chunk.hpp"
@@ -301,6 +316,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
       const int t = 16 * e + n16;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        if (2 * j + u > e) continue;   // (nothing there)
         const int s = 32 * j + 16 * u + 4 * g;
         const f32x4 v = *reinterpret_cast<const f32x4*>(&lds_t[t * LD + s]);
         const f32x4 b = *reinterpret_cast<const f32x4*>(&lds_beta[s]);
@@ -472,7 +488,7 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
       for (int j = 0; j < TS; ++j)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          tn[j][u] = load16(r, 2 * j <= wave ? (uint32_t)(C::kT + (C::fragment(wave, j) * 2 + u) * 1024 + lane * 16) : kOutside);
+          tn[j][u] = load16(r, 2 * j + u <= wave ? (uint32_t)(C::kT + (C::fragment(wave, j) * 2 + u) * 1024 + lane * 16) : kOutside);
     };
     auto fetch_decays = [&](int c) {
       const auto r = blob_of(c);
@@ -677,10 +693,11 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
       for (int j = 0; j < TS; ++j)
 #pragma unroll
         for (int q = 0; q < PY; ++q) uf[n][j][q] = both(lds_u[n][j][q], lane);
+    f32x4 y[NC][CH];
 #pragma unroll
     for (int n = 0; n < NC; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[n][r] *= to;
+      for (int i = 0; i < CH; ++i) y[n][i] = i == 0 ? o[n] * to : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < TS; ++j)
 #pragma unroll
@@ -689,8 +706,14 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
         for (int q = 0; q < PY; ++q)
 #pragma unroll
           for (int n = 0; n < NC; ++n)
-            if (p + q < PY) o[n] = mfma(uf[n][j][q], pf[j][p], o[n]);
+            if (p + q < PY) y[n][(p + 2 * q) % CH] = mfma(uf[n][j][q], pf[j][p], y[n][(p + 2 * q) % CH]);
     settle();
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      o[n] = y[n][0];
+#pragma unroll
+      for (int i = 1; i < CH; ++i) o[n] += y[n][i];
+    }
     if (__builtin_amdgcn_readfirstlane(flag | (bad < kL)) != 0)
 #pragma unroll
       for (int n = 0; n < NC; ++n)
@@ -724,8 +747,11 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
     blob += blob_step;
     __syncthreads();
     // ---- 2: S0^T Q^T (rows v, columns t)
+    f32x4 y[NC][CH];
 #pragma unroll
-    for (int n = 0; n < NC; ++n) o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) y[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       u32x4 sf[NC][PY];
@@ -739,9 +765,15 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
         for (int q = 0; q < PY; ++q)
 #pragma unroll
           for (int n = 0; n < NC; ++n)
-            if (p + q < 3) o[n] = mfma(sf[n][q], kf[i][p], o[n]);
+            if (p + q < 3) y[n][(i + p + 2 * q) % CH] = mfma(sf[n][q], kf[i][p], y[n][(i + p + 2 * q) % CH]);
     }
     settle();
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      o[n] = y[n][0];
+#pragma unroll
+      for (int i = 1; i < CH; ++i) o[n] += y[n][i];
+    }
     __syncthreads();
     // ---- 3: S <- e^{c_n} S0 + K^T (e^{c_n - c} U)
     const int flag = lds_any[par];
@@ -814,12 +846,12 @@ struct DeltaPlan {
 };
 
 // Column tiles of a workgroup. More of them share a chunk's reading, fewer leave a shorter
-// chain. A chunk takes a workgroup of one, two and four tiles 1.6, 2.45 and 4.2 us, and a
-// compute unit that has others to go on with 1.83, 1.33 and 1.31 us a tile (128 x 128
+// chain. A chunk takes a workgroup of one, two and four tiles 1.7, 2.55 and 4.4 us, and a
+// compute unit that has others to go on with 1.65, 1.33 and 1.26 us a tile (128 x 128
 // bf16): the longest sequence takes its chunks one after another, and all that the
 // 256 compute units share. By the longer of the two, us, the first tiles chosen: 8192 tokens
-// of 32 heads one 304, two 392, four 621; of 64 heads two 499, one 578, four 687; of 128 four
-// 871, two 948, one 1067.
+// of 32 heads one 301, two 382, four 613; of 64 heads two 477, one 555, four 662; of 128 four
+// 838, two 876, one 1041.
 template <typename T, int DK, int PI, int PY>
 void pick_delta(DeltaPlan& w, const rsq_linear_attn* p) {
   w.prepare = delta_prepare_kernel<T, DK, PI, PY>;
@@ -828,7 +860,7 @@ void pick_delta(DeltaPlan& w, const rsq_linear_attn* p) {
   // a sequence of len rows has ceil(len / kL) chunks; with their rows apart, at most tokens / kL + seqs in all
   w.slots = p->tokens / kL + p->seqs;
   constexpr int kMost = PI > 1 || DK > 128 ? 2 : 4;   // (four take more LDS or registers than there are)
-  constexpr float kChain[3] = {1.6f, 2.45f, 4.2f}, kTile[3] = {1.83f, 1.33f, 1.31f};
+  constexpr float kChain[3] = {1.7f, 2.55f, 4.4f}, kTile[3] = {1.65f, 1.33f, 1.26f};
   float best = 0.f;
   int nc = 0;
   for (int i = 0; 1 << i <= kMost; ++i) {

@@ -51,8 +51,10 @@ def expected(c):
 
 
 def call(c, **kw):
-    return rsq.linear_attention(c["q"], c["k"], c["v"], alpha=c["alpha"], beta=c["beta"],
-                                state=None if c["state"] is None else c["state"].clone(), offsets=c["offsets"],
+    state = None if c["state"] is None else c["state"].clone()
+    if "stream" in kw:
+        kw["stream"].wait_stream(torch.cuda.current_stream())   # for the operands, that copy among them
+    return rsq.linear_attention(c["q"], c["k"], c["v"], alpha=c["alpha"], beta=c["beta"], state=state, offsets=c["offsets"],
                                 max_len=c["max_len"], **kw)
 
 
@@ -421,7 +423,6 @@ def test_on_another_stream():
     want = call(c)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
     o, S = call(c, stream=side)
     y = rsq.linear_attention_step(S, c["q"][:1], c["k"][:1], c["v"][:1], alpha=c["alpha"][:1], beta=c["beta"][:1], stream=side)
     side.synchronize()
