@@ -2,6 +2,13 @@
 //   y[m, n] = x_scale[m] scale[n] sum_k x[m, k] code[n, k]  (+ bias[n]),
 // for the projections of prompts. Sums are exact in int32.
 //
+// Few rows read the weights: 16 x 12352 x 2048 5.2 to 5.7 us (25 MB, 4.5 to 4.9 TB/s), 32 x 28672 x
+// 8192 35 us (6.7 TB/s, some of it from the last-level cache). Many rows are bound by the matrix
+// cores and by LDS: 4096 x 28672 x 8192 takes 874 us, 2200 TOP/s, 8192^3 468 us, 2350 TOP/s, where a
+// library's int8 product takes 556. A step of 64 columns of a 256 x 256 block is 1024 cycles of
+// products on each SIMD, and 96 KB read from LDS and 32 KB written to it, which at 128
+// bytes a cycle are as many; four stages of 32 KB leave the loads three steps to arrive.
+//
 // The weights are laid out once, as products of 16 rows and 64 columns take them:
 // 1 KB each, 16 bytes a lane of a wavefront, lane (g, r) columns 16 g .. + 15 of row r.
 #include <algorithm>
@@ -311,11 +318,23 @@ struct W8Pick {
   bool large;
 };
 
-W8Pick pick_w8(int64_t m, int tiles) {
+// By the number of 16 x 16 tiles of y and the blocks of 64 columns, us (rows x n x k), the
+// first shape taken:
+//   to 600, long rows    two tiles, sixteen wavefronts: 64 x 2048 x 4096 5.3, four tiles and eight 6.4
+//   to 1300              four tiles, eight wavefronts:  40 x 3000 x 1001 4.9, two and sixteen 6.1;
+//                        16 x 12352 x 2048 5.2, blocks of 64 x 64 7.3
+//   to 2600 (1800 where  32 rows of four tiles, four wavefronts: 256 x 2048 x 4096 8.9, blocks of 64 x 64
+//   rows are short)      11.7; 333 x 1031 x 705 6.4, 10.0; but 256 x 2049 x 1025 13.0, 10.0
+//   to 9000              blocks of 64 x 64:   128 x 12352 x 2048 10.3, of 64 x 128 11.9; 512 x 4096 x 4096 16.4, 18.3
+//   above                blocks of 64 x 128:  256 x 12352 x 2048 15.7, of 64 x 64 18.0; 4096 x 12352 x 2048 141, of
+//                        256 x 256 157 (784 of them: a fourth round for 16)
+// and of 256 x 256 where those fill four fifths of the compute units' rounds: 4096 x 28672 x 8192
+// 874, 1024 x 12352 x 2048 42 (64 x 128 43.6).
+W8Pick pick_w8(int64_t m, int tiles, int kblocks) {
   const int64_t mtiles = ceil_div(m, 16), work = mtiles * tiles;
-  if (work <= 600) return {w8_few_kernel<2, 1, 16>, 16, 2, 16, false};
+  if (work <= 600 && kblocks > 32) return {w8_few_kernel<2, 1, 16>, 16, 2, 16, false};
   if (mtiles == 1 || work <= 1300) return {w8_few_kernel<4, 1, 8>, 16, 4, 8, false};
-  if (work <= 2600) return {w8_few_kernel<4, 2, 4>, 32, 4, 4, false};
+  if (work <= (kblocks > 32 ? 2600 : 1800)) return {w8_few_kernel<4, 2, 4>, 32, 4, 4, false};
   const int64_t large = ceil_div(m, 256) * ceil_div(tiles, 16), rounds = ceil_div(large, 256);
   if (large >= 160 && (rounds == 1 || large * 5 >= rounds * 256 * 4)) return {w8_kernel<256, 256, 2, 4, 4>, 256, 16, 8, true};
   if (work <= 9000) return {w8_kernel<64, 64, 2, 2, 4>, 64, 4, 4, true};
@@ -339,7 +358,7 @@ rsq_status check_w8(const rsq_w8* p, W8Layout& l) {
 
 // bytes of the rows laid out again
 size_t w8_rows_bytes(const rsq_w8* p, const W8Layout& l) {
-  if (p->m == 0 || !pick_w8(p->m, l.tiles).large || as_they_are(p)) return 0;
+  if (p->m == 0 || !pick_w8(p->m, l.tiles, l.kblocks).large || as_they_are(p)) return 0;
   return (size_t)p->m * ceil_div(p->k, 16) * 16;
 }
 
@@ -415,7 +434,7 @@ extern "C" rsq_status rsq_w8_linear(const rsq_w8* p, void* stream) {
   a.kblocks = l.kblocks, a.tiles = l.tiles;
   a.out_bf16 = p->out_dtype == RSQ_BF16;
   a.wide = aligned(p->y, 4 * osize) && p->y_stride % 4 == 0;
-  const W8Pick w = pick_w8(p->m, l.tiles);
+  const W8Pick w = pick_w8(p->m, l.tiles, l.kblocks);
   a.mt = (int32_t)ceil_div(p->m, w.rows), a.nt = (int32_t)ceil_div(l.tiles, w.tiles);
   if (!w.large) {
     hipLaunchKernelGGL(w.fn, dim3((unsigned)a.nt, (unsigned)a.mt), dim3(64 * w.waves), 0, (hipStream_t)stream, a);
