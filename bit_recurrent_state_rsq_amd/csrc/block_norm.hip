@@ -5,6 +5,12 @@
 //   h = residual + residual_scale * u, stored back rounded to its type (no residual: h = u)
 //   y = h / sqrt(mean(h^2) + eps) * next_weight (without next_weight: h), or its 8-bit codes
 // all in fp32 between the loads and the stores; each part may be left out.
+//
+// Bound by memory: every operand is read once and every result written once, a row
+// staying in registers between its sums and its output. Each part as a call of its own
+// would write u and h and read them again. 16384 x 2048 bf16 with a residual between
+// two norms (268 MB) takes 55 us, 4.9 TB/s, as much as a large copy; 16 rows of 4096,
+// normed by heads of 128, gated, to E4M3 6.0 us, of which an empty launch is 4.6.
 #include <type_traits>
 
 #include "host_util.hpp"
@@ -161,24 +167,35 @@ struct BlockPick {
   int threads, rows;
 };
 
+// A wavefront a row up to 1024 columns (its sums need no barrier), then 256, 512 and
+// 1024 threads with 8 or 16 columns each; of 32, more is read late (EARLY), which only
+// many long rows make up for by the rows a compute unit holds. us of bf16 rows with a
+// residual between two norms; of heads normed, gated, to int8: 16384 rows of 512 columns
+// 15; 19 (16 columns a thread 18; 27), 1024 24; 32 (256 threads 33; 45), 2048 42; 53 (a
+// wavefront 41; 55, 512 threads 59; 86), 4096 101; 110 (32 columns 124; 169, 1024 threads
+// 157; 185), 8192 204; 220 (256 threads 206; 221, 1024 with 16 columns 363; 475). 16384
+// columns, 512 threads against 1024: 4096 rows 117; 137 against 120; 151, 1024 rows 24;
+// 33 against 30; 37, but 256 rows 8.7; 11.6 against 7.7; 10.1. 16 rows of 2048 to 8192
+// take 5 to 7 us with any of these but 32 columns a thread, which take 1 to 3 more.
 template <typename T, int OUT>
-BlockPick pick(int cols) {
+BlockPick pick(int cols, int64_t rows) {
   if (cols <= 512) return {block_norm_kernel<T, OUT, 64, 1>, 256, 4};
   if (cols <= 1024) return {block_norm_kernel<T, OUT, 64, 2>, 256, 4};
   if (cols <= 2048) return {block_norm_kernel<T, OUT, 256, 1>, 256, 1};
   if (cols <= 4096) return {block_norm_kernel<T, OUT, 256, 2>, 256, 1};
   if (cols <= 8192) return {block_norm_kernel<T, OUT, 512, 2>, 512, 1};
+  if (cols <= 16384 && rows > 512) return {block_norm_kernel<T, OUT, 512, 4>, 512, 1};
   if (cols <= 16384) return {block_norm_kernel<T, OUT, 1024, 2>, 1024, 1};
   return {block_norm_kernel<T, OUT, 1024, 4>, 1024, 1};
 }
 
 template <typename T>
-BlockPick pick_out(int out, int cols) {
+BlockPick pick_out(int out, int cols, int64_t rows) {
   switch (out) {
-    case RSQ_F32: return pick<T, kOutF32>(cols);
-    case RSQ_BF16: return pick<T, kOutBf16>(cols);
-    case RSQ_INT8: return pick<T, kOutInt8>(cols);
-    default: return pick<T, kOutE4m3>(cols);
+    case RSQ_F32: return pick<T, kOutF32>(cols, rows);
+    case RSQ_BF16: return pick<T, kOutBf16>(cols, rows);
+    case RSQ_INT8: return pick<T, kOutInt8>(cols, rows);
+    default: return pick<T, kOutE4m3>(cols, rows);
   }
 }
 
@@ -242,7 +259,8 @@ extern "C" rsq_status rsq_block_norm(const rsq_block* p, void* stream) {
            (wide(p->residual, p->residual_stride, size, 16) ? 4 : 0) |
            (wide(p->y, p->y_stride, osize, codes ? 8 : 16) ? 8 : 0) | (aligned(p->weight, 16) ? 16 : 0) |
            (aligned(p->next_weight, 16) ? 32 : 0);
-  const BlockPick k = p->dtype == RSQ_BF16 ? pick_out<Bf16>(p->out_dtype, p->cols) : pick_out<float>(p->out_dtype, p->cols);
+  const BlockPick k = p->dtype == RSQ_BF16 ? pick_out<Bf16>(p->out_dtype, p->cols, p->rows)
+                                            : pick_out<float>(p->out_dtype, p->cols, p->rows);
   // rows beyond what one launch may have go into further ones
   const int64_t most = max_blocks(k.threads) * k.rows, scales = p->scale_group ? p->cols / p->scale_group : 1;
   for (int64_t done = 0; done < p->rows; done += most) {

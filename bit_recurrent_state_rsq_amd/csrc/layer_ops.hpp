@@ -1,6 +1,6 @@
 // Element access shared by the operators around the decode step (causal
-// convolution, selective scan, RMS norm, 4-bit-weight products): fp32 and bf16
-// activations, eight elements of a thread at a time.
+// convolution, selective scan, attention with decays, norms, 4-bit and 8-bit
+// products): fp32 and bf16 activations, eight elements of a thread at a time.
 #pragma once
 #include "rsq_device.hpp"
 

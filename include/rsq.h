@@ -456,8 +456,8 @@ rsq_status rsq_state_load(rsq_state* st, const float* dense, void* stream);
  * q, k, v, o and state are 16-byte aligned, the strides of q, k, v and o multiples
  * of 16 bytes; d_k and d_v are multiples of 8, d_v <= 4096.
  * rsq_linear_attention takes d_k <= 256 (bf16) or 128 (fp32), max_len below 2^31 -
- * 4096, rows at most 2^24 bytes apart and fewer than 2^24 workgroups (RSQ_E_UNSUPPORTED
- * beyond). With beta, sequences must not share rows: where offsets fall, results are
+ * 4096, rows at most 2^24 bytes apart and fewer than 2^24 workgroups (with beta 2^23;
+ * RSQ_E_UNSUPPORTED beyond). With beta, sequences must not share rows: where offsets fall, results are
  * unspecified. bf16: S, u and the token weights enter o as two bf16 pieces each (2^-16
  * of its terms, before o is rounded to bf16); the state itself is exact to fp32. A v
  * that is not finite makes its column NaN from its token on, a k, alpha or beta (with
