@@ -70,7 +70,7 @@ __device__ __forceinline__ int first_slot(const Sequences& q, int s, int& begin,
 
 // The sequence of a slot: the last one whose first slot is not above it. 64 sequences
 // are looked at at a time, a 64th of those left apart.
-__device__ __forceinline__ bool find_chunk(const Sequences& q, int slot, int lane, int& begin, int& len, int& chunk) {
+__device__ __forceinline__ bool find_chunk(const Sequences& q, int slot, int lane, int& sq, int& begin, int& len, int& chunk) {
   int lo = 0, n = q.seqs;
   for (;;) {
     const int step = (n + 63) / 64, s = lo + lane * step;
@@ -81,7 +81,8 @@ __device__ __forceinline__ bool find_chunk(const Sequences& q, int slot, int lan
     const int last = 63 - __builtin_clzll(hit);
     if (step == 1) {
       begin = __builtin_amdgcn_readlane(b, last), len = __builtin_amdgcn_readlane(l, last);
-      chunk = slot - (begin / kL + lo + last);
+      sq = lo + last;
+      chunk = slot - (begin / kL + sq);
       return chunk * kL < len;
     }
     n = min(step, n - last * step);
@@ -90,6 +91,123 @@ __device__ __forceinline__ bool find_chunk(const Sequences& q, int slot, int lan
 }
 
 __device__ __forceinline__ float exp2_of(double c) { return __builtin_amdgcn_exp2f((float)c); }
+
+// A sequence of up to kFew tokens (a decode batch's beside a prompt, a few drafted ones), token
+// by token with 64 columns of its state in registers, as the single-token form does: a chunk's
+// work for each would be ten times what the state's bytes take. A wavefront owns 16 columns, a
+// lane four of them and a 16th of the rows, so that no token waits for another wavefront. us so,
+// and as chunks (32 heads of 128 x 128 bf16): 256 sequences of one token 237, 863 (1080 MB, 4.6
+// TB/s), of eight 340, 875; one sequence of one 5.6, 14.4, of eight 10.8, 14.7; 255 of one beside
+// one of 16384 750, 1396; 64 of eight beside one of 64 92, 209, but one of eight beside it 20, 17.
+constexpr int kFew = 8;
+template <int DK>
+struct Few {
+  float k[kFew][DK], q[kFew][DK], v[kFew][64];
+  float alpha[kFew], beta[kFew];
+  int bad;   // the first token whose key or gates are not finite: NaN from there on
+};
+// the sum of 16 neighbouring lanes, the same in each
+__device__ __forceinline__ float sum16(float v) {
+  v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x128, 0xf, 0xf, false));
+  v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x124, 0xf, 0xf, false));
+  v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x122, 0xf, 0xf, false));
+  v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x121, 0xf, 0xf, false));
+  return v;
+}
+template <typename T, int DK>
+__device__ __forceinline__ void few_tokens(const LinearArgs& l, Few<DK>& f, int sq, int h, int64_t begin, int len) {
+  constexpr int NR = DK / 16;
+  const int tid = threadIdx.x, c = 4 * (tid >> 4), r0 = (tid & 15) * NR;
+  const int dk = l.dk, dv = l.dv, hk = h / l.per_key;
+  const T* const k = reinterpret_cast<const T*>(l.k) + begin * l.k_stride + (int64_t)hk * dk;
+  const T* const q = reinterpret_cast<const T*>(l.q) + begin * l.q_stride + (int64_t)hk * dk;
+  const T* const v = reinterpret_cast<const T*>(l.v) + begin * l.v_stride + (int64_t)h * dv;
+  T* const o = reinterpret_cast<T*>(l.o) + begin * l.o_stride + (int64_t)h * dv;
+  float* const S = l.state + ((size_t)sq * l.H + h) * dk * dv;
+  if (tid == 0) f.bad = kFew;
+  __syncthreads();
+  for (int e = tid; e < len * DK; e += 256) {
+    const int t = e / DK, r = e % DK;
+    const float kv = r < dk ? to_f32(k[t * l.k_stride + r]) : 0.f;
+    f.k[t][r] = kv;
+    f.q[t][r] = r < dk ? to_f32(q[t * l.q_stride + r]) : 0.f;
+    if (!(fabsf(kv) < __builtin_inff())) atomicMin(&f.bad, t);
+  }
+  if (tid < len) {
+    const float al = l.alpha ? l.alpha[(begin + tid) * l.alpha_stride + h] : 1.f, be = l.beta[(begin + tid) * l.beta_stride + h];
+    f.alpha[tid] = al, f.beta[tid] = be;
+    if (!(al >= 0.f && al < __builtin_inff() && fabsf(be) < __builtin_inff())) atomicMin(&f.bad, tid);
+  }
+  for (int v0 = 64 * blockIdx.y; v0 < dv; v0 += 64 * gridDim.y) {
+    const bool in = v0 + c < dv;   // (d_v is a multiple of 4)
+    float4 m[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      m[i] = l.state_in && in && r0 + i < dk ? *reinterpret_cast<const float4*>(S + (size_t)(r0 + i) * dv + v0 + c)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = tid; e < len * 64; e += 256) {
+      const int t = e >> 6, j = e & 63;
+      f.v[t][j] = v0 + j < dv ? to_f32(v[t * l.v_stride + v0 + j]) : 0.f;
+    }
+    __syncthreads();
+    // a token's factors are read while the one before is worked on
+    f32x4 kn[NR / 4], qn[NR / 4], vn;
+    float decay, beta;
+    auto read = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < NR / 4; ++i) {
+        kn[i] = *reinterpret_cast<const f32x4*>(&f.k[t][r0 + 4 * i]);
+        qn[i] = *reinterpret_cast<const f32x4*>(&f.q[t][r0 + 4 * i]);
+      }
+      vn = *reinterpret_cast<const f32x4*>(&f.v[t][c]);
+      decay = f.alpha[t], beta = f.beta[t];
+    };
+    const int bad = f.bad;
+    read(0);
+    for (int t = 0; t < len; ++t) {
+      float ks[4] = {0.f, 0.f, 0.f, 0.f}, qs[4] = {0.f, 0.f, 0.f, 0.f}, qk = 0.f;
+      float kf[NR];
+      const f32x4 vt = vn;
+      const float strength = beta;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        float* const p = &m[i].x;
+        kf[i] = kn[i / 4][i % 4];
+        const float qf = qn[i / 4][i % 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] *= decay;
+          ks[e] = __builtin_fmaf(kf[i], p[e], ks[e]);
+          qs[e] = __builtin_fmaf(qf, p[e], qs[e]);
+        }
+        qk = __builtin_fmaf(kf[i], qf, qk);
+      }
+      read(min(t + 1, len - 1));
+      qk = sum16(qk);
+      float u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = vt[e] - sum16(ks[e]);
+        u[e] = t < bad && fabsf(x) < __builtin_inff() ? strength * x : __builtin_nanf("");
+        qs[e] = sum16(qs[e]);
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        float* const p = &m[i].x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = __builtin_fmaf(kf[i], u[e], p[e]);
+      }
+      if (r0 == 0 && in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) from_f32(__builtin_fmaf(qk, u[e], qs[e]), o[t * l.o_stride + v0 + c + e]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      if (in && r0 + i < dk) *reinterpret_cast<float4*>(S + (size_t)(r0 + i) * dv + v0 + c) = m[i];
+    __syncthreads();   // v has been read
+  }
+}
 
 // One chunk of one head. K K^T and Q K^T on the matrix cores (exact products of the
 // inputs' pieces); the inverse in fp32: 16 x 16 blocks on the diagonal by
@@ -119,9 +237,15 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
   const int n16 = lane & 15, g = lane >> 4;
   const int h = blockIdx.x % a.l.H;
   const int slot = blockIdx.x / a.l.H;
-  int begin, len, chunk;
-  if (!find_chunk(a.l.s, slot, lane, begin, len, chunk)) return;
+  int sq, begin, len, chunk;
+  if (!find_chunk(a.l.s, slot, lane, sq, begin, len, chunk)) return;
   begin = __builtin_amdgcn_readfirstlane(begin), len = __builtin_amdgcn_readfirstlane(len);
+  static_assert(sizeof(Few<DK>) <= sizeof(raw), "a few tokens fit where a chunk's keys do");
+  if (len <= kFew) {
+    few_tokens<T, DK>(a.l, *reinterpret_cast<Few<DK>*>(raw), sq, h, begin, len);
+    return;
+  }
+  if (blockIdx.y > 0) return;
   const int t0 = __builtin_amdgcn_readfirstlane(chunk) * kL;
   const int hk = h / a.l.per_key, dk = a.l.dk;
   uint8_t* const blob = a.chunks + ((size_t)slot * a.l.H + h) * C::kBytes;
@@ -418,6 +542,7 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
   begin = __builtin_amdgcn_readfirstlane(begin), len = __builtin_amdgcn_readfirstlane(len);
   const int chunks = (len + kL - 1) / kL;
   if (chunks == 0 && a.l.state_in) return;
+  if (chunks == 1 && len <= kFew) return;   // (the first kernel has it)
 
   const int t16 = 16 * wave;   // its tokens
   auto rows_of = [&](int c) { return max(min(len - c * kL, kL), 0); };   // (none past the last chunk)
@@ -842,6 +967,7 @@ typedef void (*DeltaFn)(DeltaArgs);
 struct DeltaPlan {
   DeltaFn prepare, scan;
   int64_t slots, units, vblocks;
+  bool few;   // no sequence is longer than kFew
   size_t chunk_bytes, bytes;
 };
 
@@ -864,14 +990,15 @@ void pick_delta(DeltaPlan& w, const rsq_linear_attn* p) {
   float best = 0.f;
   int nc = 0;
   for (int i = 0; 1 << i <= kMost; ++i) {
-    const float shared = (float)(w.slots * p->heads) * (float)(ceil_div(tiles, 1 << i) << i) * kTile[i] / 256.f;
+    const float shared = ((float)p->tokens / kL + .5f * p->seqs) * (float)p->heads * (float)(ceil_div(tiles, 1 << i) << i) * kTile[i] / 256.f;
     const float chain = (float)ceil_div(p->max_len, kL) * kChain[i], time = chain > shared ? chain : shared;
     if (nc == 0 || time < best) best = time, nc = 1 << i;
   }
   w.scan = nc == 1 ? delta_kernel<T, DK, PI, PY, 1> : nc == 2 ? delta_kernel<T, DK, PI, PY, 2> : delta_kernel<T, DK, PI, PY, kMost>;
   w.vblocks = ceil_div(tiles, nc);
   w.chunk_bytes = (size_t)w.slots * p->heads * Chunk<PY>::kBytes;
-  w.bytes = w.chunk_bytes + (PI > 1 ? (size_t)w.slots * p->key_heads * 2 * PI * kL * DK * 2 : 0);
+  w.few = p->max_len <= kFew;
+  w.bytes = w.few ? 0 : w.chunk_bytes + (PI > 1 ? (size_t)w.slots * p->key_heads * 2 * PI * kL * DK * 2 : 0);
 }
 
 rsq_status plan_delta(const rsq_linear_attn* p, DeltaPlan& w) {
@@ -892,14 +1019,14 @@ rsq_status plan_delta(const rsq_linear_attn* p, DeltaPlan& w) {
 rsq_status delta_workspace(const rsq_linear_attn* p, size_t* bytes) {
   DeltaPlan w;
   if (const rsq_status s = plan_delta(p, w)) return s;
-  *bytes = p->max_len > 0 ? w.bytes : 0;
+  *bytes = w.bytes;
   return RSQ_OK;
 }
 
 rsq_status run_delta(const rsq_linear_attn* p, const LinearArgs& l, void* stream) {
   DeltaPlan w;
   if (const rsq_status s = plan_delta(p, w)) return s;
-  if (p->max_len > 0) {
+  if (w.bytes > 0) {
     if (!p->workspace || !aligned(p->workspace, 16)) return fail(RSQ_E_INVALID, "workspace is NULL or not 16-byte aligned");
     if (p->workspace_bytes < w.bytes)
       return fail(RSQ_E_BUFFER, "workspace has %zu bytes, the call needs %zu", p->workspace_bytes, w.bytes);
@@ -910,8 +1037,11 @@ rsq_status run_delta(const rsq_linear_attn* p, const LinearArgs& l, void* stream
   a.keys = a.chunks + w.chunk_bytes;
   a.vblocks = (int32_t)w.vblocks, a.units = (int32_t)w.units;
   if (p->max_len > 0) {
-    hipLaunchKernelGGL(w.prepare, dim3((unsigned)(w.slots * p->heads)), dim3(256), 0, (hipStream_t)stream, a);
+    // columns side by side where all sequences are short or there are few of them (a chunk takes the first only)
+    const int64_t across = w.few || w.slots * p->heads <= 512 ? ceil_div(p->d_v, 64) : 1;
+    hipLaunchKernelGGL(w.prepare, dim3((unsigned)(w.slots * p->heads), (unsigned)across), dim3(256), 0, (hipStream_t)stream, a);
     if (const rsq_status s = launched("delta rule, chunks")) return s;
+    if (w.few && (p->state_in || !p->offsets)) return RSQ_OK;   // (no chain, and no empty sequence's state to clear)
   }
   const int64_t blocks = ceil_div(w.units, 8) * 8 * w.vblocks;
   hipLaunchKernelGGL(w.scan, dim3((unsigned)blocks), dim3(512), 0, (hipStream_t)stream, a);

@@ -452,7 +452,7 @@ rsq_status rsq_state_load(rsq_state* st, const float* dense, void* stream);
  *   workspace  rsq_linear_attention_workspace bytes, 16-byte aligned (prompts only;
  *              NULL where that is 0). With beta 400 bytes a token and head, of fp32
  *              inputs 496 and 1536 a token and key head, with tokens counted in
- *              chunks of 64. Its contents need not be kept.
+ *              chunks of 64 (none with max_len up to 8). Its contents need not be kept.
  * q, k, v, o and state are 16-byte aligned, the strides of q, k, v and o multiples
  * of 16 bytes; d_k and d_v are multiples of 8, d_v <= 4096.
  * rsq_linear_attention takes d_k <= 256 (bf16) or 128 (fp32), max_len below 2^31 -

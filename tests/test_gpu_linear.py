@@ -364,6 +364,83 @@ def test_column_shapes(heads, dv):
         compare(one, o[:, h: h + 1], S[:, h: h + 1], expected(one))
 
 
+def few(c, o, S, want):
+    """Sequences of a few tokens, which round the state twice for every token: with decays and write strengths up to
+    one and keys of unit length it stays below its first norm and those of the values written."""
+    wo, wS, bo, bS = want
+    most = (0 if c["state"] is None else f64(c["state"]).norm(dim=2)) + torch.stack(
+        [f64(c["v"][a: a + n]).abs().sum(0) for a, n in c["seqs"]])
+    n = torch.tensor([n for _, n in c["seqs"]], dtype=torch.float64)[:, None, None]
+    extra = 2 * n * U * most
+    check_columns(S, wS, bS + extra, "S")
+    per = c["v"].shape[1] // c["q"].shape[1]
+    norm = f64(c["q"]).norm(dim=2).repeat_interleave(per, 1)[..., None]
+    for i, (a, n) in enumerate(c["seqs"]):
+        check(o[a: a + n], wo[a: a + n], bo[a: a + n] + norm[a: a + n] * extra[i], "o")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("state", [True, False])
+@pytest.mark.parametrize("heads,keys,dk,dv", SHAPES)
+def test_few_tokens(dtype, state, heads, keys, dk, dv):
+    """Alone, and beside sequences of one and of several chunks: the same bits."""
+    if dtype == F32 and dk > 128:
+        pytest.skip("d_k up to 128 in fp32")
+    c = make([1, 0, 8, 3, 7, 0, 5], heads, keys, dk, dv, dtype, seed=dk, first=2, gap=3, pad=8, state=state)
+    out = torch.full(c["v"].shape, 7.0, dtype=dtype, device="cuda")
+    o, S = call(c, out=out)
+    few(c, o, S, expected(c))
+    assert (o[:2] == 7.0).all() and (o[-3:] == 7.0).all(), "rows of no sequence are left as they were"
+    for i in (1, 5):
+        assert torch.equal(S[i], c["state"][i]) if state else not S[i].any()
+    d = make([1, 0, 8, 3, 7, 0, 5, 9, 64, 130], heads, keys, dk, dv, dtype, seed=dk + 1, state=state)
+    for name in ("q", "k", "v", "alpha", "beta"):
+        d[name] = d[name].clone()
+        d[name][:24] = c[name][2:26]
+    if state:
+        d["state"][:7] = c["state"]
+    o2, S2 = call(d)
+    assert torch.equal(o2[:24], o[2:26]) and torch.equal(S2[:7], S)
+    few(d, o2, S2, expected(d))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_few_tokens_of_a_batch(dtype):
+    """Without offsets: as with them, and as the token step after it goes on."""
+    c = make([4] * 5, 6, 3, 64, 72, dtype, seed=30, alpha="head")
+    o, S = call(c)
+    batch = lambda t: t.reshape(5, 4, *t.shape[1:]).contiguous()  # noqa: E731
+    o3, S3 = rsq.linear_attention(*(batch(c[n]) for n in "qkv"), alpha=c["alpha"], beta=batch(c["beta"]), state=c["state"].clone())
+    assert torch.equal(o3.reshape(20, 6, 72), o) and torch.equal(S3, S)
+    T, got = c["state"].clone(), []
+    for t in range(4):
+        got.append(rsq.linear_attention_step(T, *(batch(c[n])[:, t].contiguous() for n in "qkv"),
+                                             alpha=c["alpha"].expand(5, 6).contiguous(), beta=batch(c["beta"])[:, t].contiguous()))
+    few(c, torch.stack(got, 1).reshape(20, 6, 72), T, expected(c))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_few_tokens_that_are_not_finite(dtype):
+    """As in longer sequences: a v takes its column from its token on, a k, alpha or beta the head, a q its row."""
+    c = make([8, 6], 4, 2, 64, 40, dtype, seed=31)
+    o0, S0 = call(c)
+    bad = {**c, **{name: c[name].clone() for name in ("q", "k", "v", "alpha", "beta")}}
+    bad["v"][3, 0, 5], bad["v"][8, 1, 39] = float("inf"), float("nan")
+    bad["beta"][8, 1] = 0.0
+    c["beta"][8, 1] = 0.0
+    o0, S0 = call(c)
+    bad["k"][5, 1, 7] = float("inf")           # heads 2 and 3
+    bad["alpha"][10, 2], bad["beta"][12, 3] = -0.5, float("inf")
+    bad["q"][1, 0, 0] = float("nan")           # heads 0 and 1
+    o, S = call(bad)
+    mask = torch.zeros_like(o0, dtype=torch.bool)
+    mask[3:8, 0, 5] = mask[8:, 1, 39] = mask[5:8, 2:] = mask[10:, 2] = mask[12:, 3] = mask[1, :2] = True
+    assert torch.isnan(o[mask]).all() and torch.equal(o[~mask], o0[~mask])
+    state = torch.zeros_like(S0, dtype=torch.bool)
+    state[0, 0, :, 5] = state[1, 1, :, 39] = state[0, 2:] = state[1, 2:] = True
+    assert torch.isnan(S[state]).all() and torch.equal(S[~state], S0[~state])
+
+
 @pytest.mark.parametrize("delta", [True, False])
 def test_repeated_calls_give_the_same_bits(delta):
     c = make([700, 3, 250], 4, 2, 128, 128, BF16, seed=20, delta=delta)

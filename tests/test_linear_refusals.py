@@ -118,6 +118,8 @@ def test_attention_workspace():
     # without the delta rule short prompts need none, without rows nothing does
     assert workspace(beta=None) == 0
     assert workspace(tokens=0, max_len=0) == 0
+    # up to 8 tokens are taken one by one
+    assert workspace(seqs=1, tokens=8, max_len=8) == 0 and workspace(seqs=1, tokens=9, max_len=9) > 0
     # the documented size, and a size that follows the tokens rather than sequences x the longest one
     heads, tokens = 32, 1 << 20
     wide = dict(heads=heads, key_heads=16, d_v=128, q_stride=2048, k_stride=2048, v_stride=4096, o_stride=4096, alpha_stride=32,
