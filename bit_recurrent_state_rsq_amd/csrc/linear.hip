@@ -94,27 +94,52 @@ rsq_ssm as_scan(const rsq_linear_attn* p) {
   return s;
 }
 
+// A state of 16 MB and more, which is read and written once, is kept out of the caches: a model
+// has one for each layer, and none is still there when its next token comes. Four to 32 states in
+// turn, us so and through the caches: 32 heads of 128 x 128 of 64 sequences (134 MB) 51.5, 63, of 32
+// 25, 33, of 16 12.9, 17, of 8 9.5, 11.8; of 4 8.1, 7.3. One state alone, which stays in the
+// last-level cache, loses by it: of 64 51.5, 47.
+constexpr int64_t kPassing = 16 << 20;
+
+// (PASSES is a template's: of a branch between the two the compiler makes one plain access)
+typedef float State4 __attribute__((ext_vector_type(4)));
+template <bool PASSES>
+__device__ __forceinline__ float4 load_state(const float* p) {
+  const State4* const at = reinterpret_cast<const State4*>(p);
+  State4 v;
+  if constexpr (PASSES) v = __builtin_nontemporal_load(at);
+  else v = *at;
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+template <bool PASSES>
+__device__ __forceinline__ void store_state(float* p, const float4& m) {
+  State4* const at = reinterpret_cast<State4*>(p);
+  const State4 v = {m.x, m.y, m.z, m.w};
+  if constexpr (PASSES) __builtin_nontemporal_store(v, at);
+  else *at = v;
+}
+
 // One token: the state is read and written once (8 d_k d_v bytes a head) against 7
 // operations an element: bound by memory. With u the token's value,
 //   o = a S^T q + (k . q) u,   u = b (v - a S^T k),
 // so both sums over the rows come from one reading of the state, which stays in
-// registers until u is known. A workgroup owns 64 or 128 columns of a head's state; a thread
-// owns four consecutive columns and every 16th row. The sums meet in a fixed order. 64 sequences of 32 heads of 128 x
-// 128 (271 MB) take 61 us, 4.4 TB/s, where a large copy has 5.1; one sequence 5.1 us, of
-// which an empty launch is 4.6.
-constexpr int kRows = 16;   // rows at once
+// registers until u is known. A workgroup owns 64 columns of a head's state (128 take 55 us
+// where 64 take 51.5); a thread owns four consecutive columns and every 16th row. The sums meet
+// in a fixed order. 64 sequences of 32 heads of 128 x 128 (271 MB) take 51.5 us, 5.3 TB/s, where a
+// large copy has 5.1; one sequence 5.1 us, of which an empty launch is 4.6.
+constexpr int kColumns = 64, kRows = 16;   // of a workgroup, rows at once
 
-template <typename T, int NR, int COLS>   // columns of a workgroup: 64 or 128
-__global__ __launch_bounds__(COLS / 4 * kRows) void linear_step_kernel(LinearArgs a, int32_t vblocks) {
-  constexpr int FOURS = COLS / 4, WAVES = FOURS * kRows / 64;
-  __shared__ float part[WAVES][2][COLS], part_qk[WAVES];
+template <typename T, int NR, bool PASSES>
+__global__ __launch_bounds__(kColumns / 4 * kRows) void linear_step_kernel(LinearArgs a, int32_t vblocks) {
+  constexpr int FOURS = kColumns / 4, WAVES = FOURS * kRows / 64;
+  __shared__ float part[WAVES][2][kColumns], part_qk[WAVES];
   const int64_t id = blockIdx.x / vblocks;
   const int vb = blockIdx.x % vblocks;
   const int h = (int)(id % a.H);
   const int64_t s = id / a.H;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = threadIdx.x % FOURS, r0 = threadIdx.x / FOURS;
-  const int col = vb * COLS + 4 * c;
+  const int col = vb * kColumns + 4 * c;
   const bool in = col < a.dv;   // (d_v is a multiple of 4)
   const T* q = reinterpret_cast<const T*>(a.q) + s * a.q_stride + (int64_t)(h / a.per_key) * a.dk;
   const T* k = reinterpret_cast<const T*>(a.k) + s * a.k_stride + (int64_t)(h / a.per_key) * a.dk;
@@ -125,7 +150,7 @@ __global__ __launch_bounds__(COLS / 4 * kRows) void linear_step_kernel(LinearArg
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int row = r0 + i * kRows;
-    m[i] = row < a.dk && in && a.state_in ? *reinterpret_cast<const float4*>(S + (size_t)row * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    m[i] = row < a.dk && in && a.state_in ? load_state<PASSES>(S + (size_t)row * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
     kf[i] = row < a.dk ? to_f32(k[row]) : 0.f;
     qf[i] = row < a.dk ? to_f32(q[row]) : 0.f;
   }
@@ -179,7 +204,7 @@ __global__ __launch_bounds__(COLS / 4 * kRows) void linear_step_kernel(LinearArg
       float* p = &m[i].x;
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[e] = __builtin_fmaf(kf[i], u[e], p[e]);
-      *reinterpret_cast<float4*>(S + (size_t)row * a.dv) = m[i];
+      store_state<PASSES>(S + (size_t)row * a.dv, m[i]);
     }
   }
   if (r0 == 0) {
@@ -190,9 +215,9 @@ __global__ __launch_bounds__(COLS / 4 * kRows) void linear_step_kernel(LinearArg
 }
 
 typedef void (*LinearStepFn)(LinearArgs, int32_t);
-template <typename T, int COLS>
+template <typename T, bool PASSES>
 LinearStepFn pick_step(int dk) {
-  return dk <= 64 ? linear_step_kernel<T, 4, COLS> : dk <= 128 ? linear_step_kernel<T, 8, COLS> : linear_step_kernel<T, 16, COLS>;
+  return dk <= 64 ? linear_step_kernel<T, 4, PASSES> : dk <= 128 ? linear_step_kernel<T, 8, PASSES> : linear_step_kernel<T, 16, PASSES>;
 }
 
 }  // namespace
@@ -219,15 +244,13 @@ extern "C" rsq_status rsq_linear_attention(const rsq_linear_attn* p, void* strea
 extern "C" rsq_status rsq_linear_attention_step(const rsq_linear_attn* p, void* stream) {
   if (const rsq_status s = check_linear(p, false)) return s;
   if (const rsq_status s = check_linear_memory(p)) return s;
-  // 128 columns where there are workgroups for four on each of 256 compute units: 64 tokens of 32
-  // heads of 128 x 128 61 us (64 columns 63), one token 6.2 (5.2).
-  const int cols = p->d_v <= 64 || (int64_t)p->seqs * p->heads * ceil_div(p->d_v, 128) < 1024 ? 64 : 128;
-  const int threads = cols / 4 * kRows;
-  const int64_t vblocks = ceil_div(p->d_v, cols);
+  constexpr int threads = kColumns / 4 * kRows;
+  const int64_t vblocks = ceil_div(p->d_v, kColumns);
   const int64_t blocks = (int64_t)p->seqs * p->heads * vblocks;
   if (const rsq_status s = check_blocks(blocks, threads)) return s;
-  const LinearStepFn fn = p->dtype == RSQ_BF16 ? (cols == 64 ? pick_step<Bf16, 64>(p->d_k) : pick_step<Bf16, 128>(p->d_k))
-                                               : (cols == 64 ? pick_step<float, 64>(p->d_k) : pick_step<float, 128>(p->d_k));
+  const bool passes = (int64_t)p->seqs * p->heads * p->d_k * p->d_v * 4 >= kPassing;
+  const LinearStepFn fn = p->dtype == RSQ_BF16 ? (passes ? pick_step<Bf16, true> : pick_step<Bf16, false>)(p->d_k)
+                                               : (passes ? pick_step<float, true> : pick_step<float, false>)(p->d_k);
   hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(threads), 0, (hipStream_t)stream, linear_args(p), (int32_t)vblocks);
   return launched("linear attention step");
 }
