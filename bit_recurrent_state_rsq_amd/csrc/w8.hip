@@ -8,6 +8,9 @@
 // library's int8 product takes 556. A step of 64 columns of a 256 x 256 block is 1024 cycles of
 // products on each SIMD, and 96 KB read from LDS and 32 KB written to it, which at 128
 // bytes a cycle are as many; four stages of 32 KB leave the loads three steps to arrive.
+// A block of 128 x 256 has 512 cycles of products and 88 KB (704 cycles) of LDS, but two of
+// them fit a compute unit and shorter rows lose less at their ends: 4096 x 12352 x 2048 115 to 122 us,
+// 1750 TOP/s, where the library's product takes 119 to 126.
 //
 // The weights are laid out once, as products of 16 rows and 64 columns take them:
 // 1 KB each, 16 bytes a lane of a wavefront, lane (g, r) columns 16 g .. + 15 of row r.
@@ -326,17 +329,22 @@ struct W8Pick {
 //   to 2600 (1800 where  32 rows of four tiles, four wavefronts: 256 x 2048 x 4096 8.9, blocks of 64 x 64
 //   rows are short)      11.7; 333 x 1031 x 705 6.4, 10.0; but 256 x 2049 x 1025 13.0, 10.0
 //   to 9000              blocks of 64 x 64:   128 x 12352 x 2048 10.3, of 64 x 128 11.9; 512 x 4096 x 4096 16.4, 18.3
-//   above                blocks of 64 x 128:  256 x 12352 x 2048 15.7, of 64 x 64 18.0; 4096 x 12352 x 2048 141, of
-//                        256 x 256 157 (784 of them: a fourth round for 16)
-// and of 256 x 256 where those fill four fifths of the compute units' rounds: 4096 x 28672 x 8192
-// 874, 1024 x 12352 x 2048 42 (64 x 128 43.6).
+//   above                blocks of 64 x 128:  256 x 12352 x 2048 15.0, of 64 x 64 18.2
+// Before the last two come blocks of 128 x 256, three stages of 24 KB, two workgroups a compute
+// unit, where there are workgroups for three quarters of the units and rows of more than 1024: 4096 x
+// 12352 x 2048 115, of 64 x 128 142, of 256 x 256 165; 512 x 12352 x 2048 25.3, 29.6, 43; but 700 x
+// 7000 x 1024 (168 workgroups) 15.9, 13.4 and 4096 x 28672 x 1024 238, 224 (y is most of it);
+// and of 256 x 256 where rows are longer than 6144 and those blocks fill four fifths of the compute
+// units' rounds: 4096 x 28672 x 8192 882, of 128 x 256 954; 512 x 28672 x 8192 117, 138; but 4096 x
+// 8192 x 6144 197, 184.
 W8Pick pick_w8(int64_t m, int tiles, int kblocks) {
   const int64_t mtiles = ceil_div(m, 16), work = mtiles * tiles;
   if (work <= 600 && kblocks > 32) return {w8_few_kernel<2, 1, 16>, 16, 2, 16, false};
   if (mtiles == 1 || work <= 1300) return {w8_few_kernel<4, 1, 8>, 16, 4, 8, false};
   if (work <= (kblocks > 32 ? 2600 : 1800)) return {w8_few_kernel<4, 2, 4>, 32, 4, 4, false};
   const int64_t large = ceil_div(m, 256) * ceil_div(tiles, 16), rounds = ceil_div(large, 256);
-  if (large >= 160 && (rounds == 1 || large * 5 >= rounds * 256 * 4)) return {w8_kernel<256, 256, 2, 4, 4>, 256, 16, 8, true};
+  if (kblocks > 96 && large * 5 >= rounds * 256 * 4) return {w8_kernel<256, 256, 2, 4, 4>, 256, 16, 8, true};
+  if (kblocks > 16 && ceil_div(m, 128) * ceil_div(tiles, 16) >= 190) return {w8_kernel<128, 256, 2, 4, 3>, 128, 16, 8, true};
   if (work <= 9000) return {w8_kernel<64, 64, 2, 2, 4>, 64, 4, 4, true};
   return {w8_kernel<64, 128, 2, 2, 4>, 64, 8, 4, true};
 }

@@ -215,6 +215,19 @@ def test_w8_strides_and_alignment(m, n, k, stride, shift):
     compare_w8(*w8_case(m, n, k, stride=stride, shift=shift), "f32")
 
 
+@pytest.mark.parametrize("m,n,k", [(1500, 4100, 1104), (1500, 4100, 1101), (3300, 4090, 6208), (3300, 4090, 6201)])
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_w8_of_large_blocks(m, n, k, out_dtype):
+    """Blocks of 128 x 256, and of 256 x 256 with long rows; the sums are whole numbers, exact in fp64 on the GPU."""
+    x, codes, scales, xs, bias = w8_case(m, n, k, seed=k)
+    y = rsq.w8_linear(x, rsq.W8Weight(codes, scales), xs, bias=bias, out_dtype=out_dtype)
+    want = (x.double() @ codes.double().t().contiguous()) * xs.double()[:, None] * scales.double()
+    bound = 3.05 * U * want.abs()
+    want = want + bias.double()
+    bound += 1.05 * U * want.abs() + 1e-37 + half(BF16 if out_dtype == "bf16" else F32) * want.abs()
+    assert bool(((y.double() - want).abs() <= bound).all())
+
+
 def test_w8_largest_sums():
     """The longest row of -128 by -128 that int32 holds."""
     k = (1 << 17) - 1
