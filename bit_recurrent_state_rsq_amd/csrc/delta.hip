@@ -10,7 +10,7 @@
 // follows the state through a sequence's chunks.
 //
 // 16384 tokens of 32 heads of 128 x 128 with 16 key heads (bf16, 411 MB, 60 GFLOP of the
-// recurrence's own operations: 80 us) take 511 us: 99 for the chunks, which is memory (32 KB
+// recurrence's own operations: 80 us) take 511 to 523 us (by the card): 99 for the chunks, which is memory (32 KB
 // read, 25 written a chunk and head, 4.7 TB/s), and 410 for the chain of 256 chunks. A chunk of it
 // takes 1.6 us, three steps of about 1100 cycles: in the first the state's pieces come
 // through LDS (64 KB for eight wavefronts), in the second the products with T, in the third
