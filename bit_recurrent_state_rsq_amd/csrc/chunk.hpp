@@ -44,6 +44,17 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[N]) {
   }
 }
 
+// Three pieces of which the first is cut, and so never overflows, and the second rounded: what
+// two of them leave is of either sign and at most 2^-16 of the value, where two cut ones leave up
+// to 2^-15, always towards zero. The six leading products of such pieces leave out 3.1 x 2^-24 of
+// the whole at most, 0.4 in the mean square and nothing in the mean (of cut ones 7.8, 1.5 and 1.1).
+__device__ __forceinline__ void split_even(float a, float b, uint32_t (&p)[3]) {
+  p[0] = high_pair(a, b);
+  a -= __uint_as_float(__float_as_uint(a) & 0xFFFF0000u), b -= __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
+  p[1] = bf16_pair(a, b);
+  p[2] = high_pair(a - low_half(p[1]), b - high_half(p[1]));   // (eight bits are left)
+}
+
 // A chunk's rows as a buffer: one scalar base, 32-bit offsets, and rows past the
 // sequence's end out of its range, where loads give zeros and stores are dropped.
 // Offsets of lanes without a row or column of their own start at kOutside. All of
@@ -80,6 +91,7 @@ struct Vec8 {
     for (int i = 0; i < (PI == 1 ? 1 : 2); ++i)
       raw[i] = __builtin_amdgcn_raw_buffer_load_b128(r.rsrc, (int)(offset + 16 * i), 0, 0);
   }
+  template <bool EVEN = false>
   __device__ __forceinline__ void pieces(u32x4 (&out)[PI]) const {
     if constexpr (PI == 1) {
       out[0] = raw[0];
@@ -87,7 +99,9 @@ struct Vec8 {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t p[PI];
-        split_pair<PI>(__uint_as_float(raw[w >> 1][2 * (w & 1)]), __uint_as_float(raw[w >> 1][2 * (w & 1) + 1]), p);
+        const float a = __uint_as_float(raw[w >> 1][2 * (w & 1)]), b = __uint_as_float(raw[w >> 1][2 * (w & 1) + 1]);
+        if constexpr (EVEN) split_even(a, b, p);
+        else split_pair<PI>(a, b, p);
 #pragma unroll
         for (int i = 0; i < PI; ++i) out[i][w] = p[i];
       }

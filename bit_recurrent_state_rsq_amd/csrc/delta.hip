@@ -90,6 +90,10 @@ __device__ __forceinline__ bool find_chunk(const Sequences& q, int slot, int lan
   }
 }
 
+// Three pieces of factors that reach the state, two of those that reach bf16 outputs only
+__device__ __forceinline__ void split(float a, float b, uint32_t (&p)[3]) { split_even(a, b, p); }
+__device__ __forceinline__ void split(float a, float b, uint32_t (&p)[2]) { split_pair<2>(a, b, p); }
+
 __device__ __forceinline__ float exp2_of(double c) { return __builtin_amdgcn_exp2f((float)c); }
 
 // A sequence of up to kFew tokens (a decode batch's beside a prompt, a few drafted ones), token
@@ -279,8 +283,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
     const int row = row0 + i * RB;
     const uint32_t at = TB::at(row, piece);
     u32x4 pk[PI], pq[PI];
-    rk[i].pieces(pk);
-    rq[i].pieces(pq);
+    rk[i].template pieces<true>(pk);
+    rq[i].template pieces<true>(pq);
 #pragma unroll
     for (int p = 0; p < PI; ++p) {
       *reinterpret_cast<u32x4*>(lds_k + p * BB + at) = pk[p];
@@ -379,8 +383,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t lo[PY], hi[PY];
-        split_pair<PY>(p[j][u][0], p[j][u][1], lo);
-        split_pair<PY>(p[j][u][2], p[j][u][3], hi);
+        split(p[j][u][0], p[j][u][1], lo);
+        split(p[j][u][2], p[j][u][3], hi);
 #pragma unroll
         for (int q = 0; q < PY; ++q) pf[q][2 * u] = lo[q], pf[q][2 * u + 1] = hi[q];
       }
@@ -488,8 +492,8 @@ __device__ __forceinline__ u32x4 both(const Halves& h, int lane) {
 template <int N>
 __device__ __forceinline__ void put_four(Halves (&h)[N], int half, int lane, const f32x4& v) {
   uint32_t lo[N], hi[N];
-  split_pair<N>(v[0], v[1], lo);
-  split_pair<N>(v[2], v[3], hi);
+  split(v[0], v[1], lo);
+  split(v[2], v[3], hi);
 #pragma unroll
   for (int q = 0; q < N; ++q) h[q][half][lane] = u32x2{lo[q], hi[q]};
 }
@@ -627,8 +631,8 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
         for (int u = 0; u < 2; ++u) {
           const f32x4 v = __builtin_bit_cast(f32x4, tn[j][u]);
           uint32_t lo[kPieces], hi[kPieces];
-          split_pair<kPieces>(v[0], v[1], lo);
-          split_pair<kPieces>(v[2], v[3], hi);
+          split(v[0], v[1], lo);
+          split(v[2], v[3], hi);
 #pragma unroll
           for (int q = 0; q < kPieces; ++q) tf[j][q][2 * u] = lo[q], tf[j][q][2 * u + 1] = hi[q];
         }
@@ -831,7 +835,8 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs a) {
         for (int q = 0; q < PY; ++q)
 #pragma unroll
           for (int n = 0; n < NC; ++n)
-            if (p + q < PY) y[n][(p + 2 * q) % CH] = mfma(uf[n][j][q], pf[j][p], y[n][(p + 2 * q) % CH]);
+            // (of two pieces each all four: without the last 2^-16 more of a term could be missing)
+            if (p + q < 3) y[n][(p + 2 * q) % CH] = mfma(uf[n][j][q], pf[j][p], y[n][(p + 2 * q) % CH]);
     settle();
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
