@@ -123,7 +123,8 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void block_norm_kernel(BlockArgs
         }
       }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) rstd[i] = 1.f / sqrtf(sums[i] / (float)a.group + a.eps);
+      for (int i = 0; i < NV; ++i)   // (threads without columns stay at zero, with an eps of zero too)
+        rstd[i] = (i * R + tid) * kCols < a.cols ? 1.f / sqrtf(sums[i] / (float)a.group + a.eps) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
