@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from layer_reference import H, U, check, f64
+from test_gpu_linear import compare, compare_step, expected, make
 
 pytestmark = pytest.mark.gpu
 
@@ -14,7 +15,8 @@ rsq = None
 @pytest.fixture(scope="module", autouse=True)
 def _package():
     global rsq
-    rsq = pytest.importorskip("bit_recurrent_state_rsq_amd")
+    import test_gpu_linear
+    rsq = test_gpu_linear.rsq = pytest.importorskip("bit_recurrent_state_rsq_amd")
     assert torch.cuda.is_available()
 
 
@@ -78,3 +80,52 @@ def test_products_of_pieces_leave_out_either_sign():
     off = (f64(o) - want) / want
     assert off.abs().max() < 12 * U
     assert off.mean().abs() < 0.3 * U, off.mean() / U
+
+
+# ---------------------------------------------------------------- kernels of their own
+
+def framed(t, value):
+    """A copy of t with a row of `value` before and behind it, and the frame."""
+    buf = torch.full((t.shape[0] + 2,) + tuple(t.shape[1:]), value, dtype=t.dtype, device="cuda")
+    buf[1:-1] = t
+    return buf[1:-1], buf
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [
+    (BF16, 64, 72), (BF16, 40, 72), (BF16, 128, 72), (BF16, 120, 72), (BF16, 256, 72), (BF16, 200, 104),   # two column tiles a workgroup
+    (F32, 64, 72), (F32, 40, 104), (F32, 128, 72), (F32, 120, 104),
+    (BF16, 64, 104), (BF16, 24, 104), (BF16, 128, 104), (BF16, 72, 104)])                                  # four
+@pytest.mark.parametrize("state", [True, False])
+def test_workgroups_of_several_column_tiles(dtype, dk, dv, state):
+    """Many heads: two or four column tiles a workgroup, the last of which have no columns, or eight of them. Sums are added
+    in another order than by one tile a workgroup: each is held to the definition, and what surrounds the outputs stays."""
+    heads, keys, lengths = 300, 3, [100, 40]
+    c = make(lengths, heads, keys, dk, dv, dtype, seed=dk + dv, first=2, gap=3, pad=8, state=state)
+    wide = torch.full((c["v"].shape[0], heads * dv + 16), 7.0, dtype=dtype, device="cuda")
+    out = wide[:, 8: 8 + heads * dv].view(-1, heads, dv)
+    S, frame = framed(c["state"], 5.0) if state else (None, None)
+    o, S = rsq.linear_attention(c["q"], c["k"], c["v"], alpha=c["alpha"], beta=c["beta"], state=S, offsets=c["offsets"],
+                                max_len=c["max_len"], out=out)
+    for h in (0, 157, 299):
+        g = h // (heads // keys)
+        one = {**c, "q": c["q"][:, g: g + 1], "k": c["k"][:, g: g + 1], "v": c["v"][:, h: h + 1], "alpha": c["alpha"][:, h: h + 1],
+               "beta": c["beta"][:, h: h + 1], "state": c["state"][:, h: h + 1] if state else None}
+        compare(one, o[:, h: h + 1], S[:, h: h + 1], expected(one))
+    assert (wide[:, :8] == 7.0).all() and (wide[:, -8:] == 7.0).all() and (o[:2] == 7.0).all() and (o[-3:] == 7.0).all()
+    if state:
+        assert (frame[0] == 5.0).all() and (frame[-1] == 5.0).all()
+    assert torch.isfinite(S).all() and torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("delta", [True, False])
+@pytest.mark.parametrize("dk,dv", [(64, 40), (24, 136), (72, 104), (128, 72), (200, 40), (256, 200)])
+def test_steps_on_states_past_the_caches(dtype, delta, dk, dv):
+    """States of 16 MB and more, which are read and written past the caches."""
+    heads = 16
+    seqs = -(-(1 << 24) // (heads * dk * dv * 4))
+    c = make([1] * seqs, heads, 4, dk, dv, dtype, seed=dk + dv, pad=8, delta=delta)
+    S, frame = framed(c["state"], 5.0)
+    o = rsq.linear_attention_step(S, c["q"], c["k"], c["v"], alpha=c["alpha"], beta=c["beta"])
+    compare_step(c, o, S)
+    assert (frame[0] == 5.0).all() and (frame[-1] == 5.0).all()
