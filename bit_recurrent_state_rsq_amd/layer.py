@@ -150,8 +150,8 @@ def linear_attention(q, k, v, alpha=None, beta=None, state=None, offsets=None, m
     S = alpha S + k u^T with u = v, or with write strengths beta the delta rule u = beta (v - alpha S^T k); o = S^T q.
     v: [sequences, tokens, heads, d_v] (or packed [tokens, ...] with offsets and max_len, as causal_conv); q, k:
     [..., key heads, d_k], shared by heads / key heads each; alpha, beta: fp32 [..., heads], alpha also [heads] for all
-    tokens, or None for 1. state: fp32 [sequences, heads, d_k, d_v] to start from, updated in place; None starts from
-    zero and makes one. State.load_dense takes it for the decode step."""
+    tokens, or None for 1. An alpha of 0 clears what is finite of a state. state: fp32 [sequences, heads, d_k, d_v] to
+    start from, updated in place; None starts from zero and makes one. State.load_dense takes it for the decode step."""
     return _run(_binding.attention, v, stream, q, k, v, alpha, beta, state, offsets, max_len, out)
 
 

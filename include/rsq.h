@@ -444,7 +444,9 @@ rsq_status rsq_state_load(rsq_state* st, const float* dense, void* stream);
  *   dtype      RSQ_F32 | RSQ_BF16: q, k, v, o
  *   q, k       device [tokens][key_heads][d_k];  v, o device [tokens][heads][d_v]
  *   alpha      device fp32 [tokens][heads], not negative; alpha_stride 0: [heads], the
- *              same for all tokens; NULL: 1. An alpha of 0 clears the state
+ *              same for all tokens; NULL: 1. An alpha of 0 clears a finite state; a
+ *              column that is not finite stays so (0 times an infinity is a NaN): to
+ *              drop a state whatever it holds, start from zero with state_in 0
  *   beta       device fp32 [tokens][heads]; NULL: no delta rule
  *   state      device fp32 [seqs][heads][d_k][d_v], replaced by the state after
  *              each sequence. state_in 0: start from zero, the contents are not

@@ -129,3 +129,26 @@ def test_steps_on_states_past_the_caches(dtype, delta, dk, dv):
     o = rsq.linear_attention_step(S, c["q"], c["k"], c["v"], alpha=c["alpha"], beta=c["beta"])
     compare_step(c, o, S)
     assert (frame[0] == 5.0).all() and (frame[-1] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens", [1, 5, 20, 150])
+@pytest.mark.parametrize("delta", [True, False])
+def test_states_that_are_not_finite(dtype, tokens, delta):
+    """A state's column that is not finite gives no finite o, also where a decay of zero clears what is finite (0 times an
+    infinity is a NaN); other columns keep their bits. A state that is to be dropped is left out."""
+    c = make([tokens] * 2, 2, 1, 64, 40, dtype, seed=tokens, delta=delta)
+    c["alpha"][0] = 0.0
+    k = c["k"]
+    k[k == 0] = 1.0
+    args = dict(alpha=c["alpha"], beta=c["beta"], offsets=c["offsets"], max_len=c["max_len"])
+    o0, S0 = rsq.linear_attention(c["q"], k, c["v"], state=c["state"].clone(), **args)
+    bad = c["state"].clone()
+    bad[0, 1, 7, 3], bad[1, 0, 9, 39] = float("inf"), float("nan")
+    o, S = rsq.linear_attention(c["q"], k, c["v"], state=bad, **args)
+    mask = torch.zeros_like(o0, dtype=torch.bool)
+    mask[:tokens, 1, 3] = mask[tokens:, 0, 39] = True
+    state = torch.zeros_like(S0, dtype=torch.bool)
+    state[0, 1, :, 3] = state[1, 0, :, 39] = True
+    assert not torch.isfinite(o[mask]).any() and torch.equal(o[~mask], o0[~mask]) and torch.equal(S[~state], S0[~state])
+    assert not torch.isfinite(S[0, 1, 7, 3]) and torch.isnan(S[1, 0, 9, 39])
