@@ -5,7 +5,7 @@ import torch
 
 import linear_reference as ref
 from layer_reference import U, check, f64
-from test_gpu_block import BF16, F32, half, norm_case, run_norm
+from test_gpu_block import BF16, F32, compare, half, norm_case, run_norm
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,21 @@ def test_norm_without_eps(cols, group, out):
         s = f64(scales)
         step = 0.5 * s if out == "int8" else torch.maximum(want.abs() * 2.0 ** -4, s * 2.0 ** -10)
         check(f64(codes) * s, want, step * (1 + 8 * U) + by * (1 + 2.0 ** -3) + 4 * U * want.abs(), "codes")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,cols,group,gate", [(600, 16384, 0, "after"), (513, 8200, 0, "before"), (513, 8200, 1640, "after"),
+                                                  (520, 9216, 1152, "before"), (515, 16384, 4096, None), (514, 12288, 128, "after")])
+def test_norm_of_many_long_rows(dtype, rows, cols, group, gate):
+    """More than 512 rows of 8193 to 16384 columns: 32 columns a thread, gate and residual read where they are used."""
+    compare(norm_case(rows, cols, dtype, group=group, gate=gate, seed=rows), out_dtype="f32")
+
+
+def test_norm_of_many_long_rows_to_codes():
+    c = norm_case(515, 8200, BF16, group=1640, seed=2)
+    (codes, scales), res = run_norm(c, out_dtype="int8")
+    want, h, by, bh = definition(c, 1e-5)
+    check(res, h, bh + half(BF16) * h.abs(), "residual")
+    largest, s = want.abs().amax(1, keepdim=True), f64(scales)
+    check(scales, largest / 127, by.amax(1, keepdim=True) / 127 + 2 * U * largest / 127, "scales")
+    check(f64(codes) * s, want, 0.5 * s * (1 + 8 * U) + by * (1 + 2.0 ** -3) + 4 * U * want.abs(), "codes")
