@@ -1,22 +1,25 @@
 """Norms around a block and products of 8-bit integers at the sizes and arguments where a kernel of their own, or threads
 without columns, take part."""
+import ctypes
+
 import pytest
 import torch
 
 import linear_reference as ref
 from layer_reference import U, check, f64
-from test_gpu_block import BF16, F32, compare, half, norm_case, run_norm
+from test_gpu_block import BF16, F32, compare, compare_w8, half, norm_case, run_norm, w8_case
 
 pytestmark = pytest.mark.gpu
 
-rsq = None
+rsq = _abi = None
 
 
 @pytest.fixture(scope="module", autouse=True)
 def _package():
-    global rsq
+    global rsq, _abi
     import test_gpu_block
     rsq = test_gpu_block.rsq = pytest.importorskip("bit_recurrent_state_rsq_amd")
+    from bit_recurrent_state_rsq_amd import _abi
     assert torch.cuda.is_available()
 
 
@@ -69,3 +72,58 @@ def test_norm_of_many_long_rows_to_codes():
     largest, s = want.abs().amax(1, keepdim=True), f64(scales)
     check(scales, largest / 127, by.amax(1, keepdim=True) / 127 + 2 * U * largest / 127, "scales")
     check(f64(codes) * s, want, 0.5 * s * (1 + 8 * U) + by * (1 + 2.0 ** -3) + 4 * U * want.abs(), "codes")
+
+
+# ---------------------------------------------------------------- 8-bit products
+
+# rows x n x k that take 32 rows and four tiles a workgroup, and blocks of 64 x 64
+FEW = [(333, 1031, 705), (256, 2048, 2100), (270, 1500, 96), (100, 3700, 1000), (257, 2001, 2049)]
+BLOCKS = [(130, 4100, 200), (128, 12352, 100), (100, 4500, 333), (40, 12352, 1000), (520, 4096, 96), (1000, 1024, 256), (300, 2400, 65)]
+
+
+@pytest.mark.parametrize("m,n,k", FEW + BLOCKS)
+@pytest.mark.parametrize("out_dtype,bias", [("bf16", True), ("f32", False)])
+def test_w8_of_a_few_hundred_rows(m, n, k, out_dtype, bias):
+    compare_w8(*w8_case(m, n, k, bias, seed=m + n), out_dtype)
+
+
+@pytest.mark.parametrize("m,n,k", [(270, 1500, 96), (300, 2400, 96)])
+@pytest.mark.parametrize("stride,shift", [(112, 0), (97, 0), (96, 1), (112, 8), (128, 16)])
+def test_w8_of_a_few_hundred_rows_strides_and_alignment(m, n, k, stride, shift):
+    x, codes, scales, xs, bias = w8_case(m, n, k, stride=stride, shift=shift)
+    out = torch.full((m + 2, n + 9), 7.0, device="cuda")
+    y = rsq.w8_linear(x, rsq.W8Weight(codes, scales), xs, bias=bias, out=out[1: m + 1, 4: n + 4], out_dtype="f32")
+    want, bound = ref.w8(x, codes, scales, xs, bias)
+    check(y, want, bound + U * want.abs(), "y")
+    assert (out[0] == 7.0).all() and (out[-1] == 7.0).all() and (out[:, :4] == 7.0).all() and (out[:, n + 4:] == 7.0).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(300, 2400, 65), (1500, 4100, 1101), (2600, 4096, 90)])
+def test_w8_with_a_workspace_captured_and_replayed(m, n, k):
+    """Rows that do not begin at multiples of 16 bytes and are laid out again, in blocks of 64 x 64, 128 x 256 and 64 x 128: two
+    graphs, replayed in turn with eager calls between them, each against the definition."""
+    cases = [w8_case(m, n, k, seed=s) for s in (1, 2)]
+    need = ctypes.c_size_t()
+    p = _abi.W8(out_dtype=_abi.BF16, m=m, n=n, k=k, x=cases[0][0].data_ptr(), x_stride=k, y_stride=n)
+    assert _abi.lib.rsq_w8_workspace(ctypes.byref(p), ctypes.byref(need)) == 0 and need.value > 0
+    ws = [rsq.W8Weight(c[1], c[2]) for c in cases]
+    run = lambda i: rsq.w8_linear(cases[i][0], ws[i], cases[i][3], bias=cases[i][4])  # noqa: E731
+    want = [run(i).clone() for i in (0, 1)]
+    for c, y in zip(cases, want):
+        # (whole numbers, of which fp64 holds every sum)
+        exact = (c[0].double() @ c[1].double().t().contiguous()) * c[3].double()[:, None] * c[2].double()
+        bound = 3.05 * U * exact.abs()
+        exact = exact + c[4].double()
+        assert bool(((y.double() - exact).abs() <= bound + (1.05 * U + half(BF16)) * exact.abs() + 1e-37).all())
+    graphs, made = [torch.cuda.CUDAGraph() for _ in (0, 1)], [None, None]
+    for i in (0, 1):
+        with torch.cuda.graph(graphs[i]):
+            made[i] = run(i)
+    for _ in range(3):
+        for y in made:
+            y.zero_()
+        for g in graphs:
+            g.replay()
+        eager = [run(i) for i in (0, 1)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(made[i], want[i]) and torch.equal(eager[i], want[i]) for i in (0, 1))
