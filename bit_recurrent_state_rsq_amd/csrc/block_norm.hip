@@ -170,14 +170,16 @@ struct BlockPick {
 
 // A wavefront a row up to 1024 columns (its sums need no barrier), then 256, 512 and
 // 1024 threads with 8 or 16 columns each; of 32, more is read late (EARLY), which only
-// many long rows make up for by the rows a compute unit holds. us of bf16 rows with a
-// residual between two norms; of heads normed, gated, to int8: 16384 rows of 512 columns
-// 15; 19 (16 columns a thread 18; 27), 1024 24; 32 (256 threads 33; 45), 2048 42; 53 (a
-// wavefront 41; 55, 512 threads 59; 86), 4096 101; 110 (32 columns 124; 169, 1024 threads
-// 157; 185), 8192 204; 220 (256 threads 206; 221, 1024 with 16 columns 363; 475). 16384
-// columns, 512 threads against 1024: 4096 rows 117; 137 against 120; 151, 1024 rows 24;
-// 33 against 30; 37, but 256 rows 8.7; 11.6 against 7.7; 10.1. 16 rows of 2048 to 8192
-// take 5 to 7 us with any of these but 32 columns a thread, which take 1 to 3 more.
+// more long rows than there are compute units make up for: two are then on a unit. us of
+// bf16 rows with a residual between two norms; of heads normed, gated, to int8, on operands
+// past the last-level cache: 16384 rows of 512 columns 18; 20 (16 columns a thread 21; 26),
+// 1024 31; 33 (256 threads 41; 49), 2048 53; 60 (a wavefront 59; 61, 512 threads 77; 94),
+// 4096 103; 112 (512 threads 103; 116, 1024 156; 193), 8192 204; 218 (256 threads 206; 219,
+// 1024 209; 240). 16384 columns, 512 threads against 1024: 4096 rows 112; 126 against 121;
+// 152, 512 rows 18; 21 against 20; 23, 257 rows 13; 19 against 17; 21, but 256 rows 12.4;
+// 14.9 against 11.3; 12.6. 16 rows of 2048 columns 3.8; 4.5 (a wavefront 5.2; 8.5), of 4096
+// 4.3; 6.0 (512 threads 3.9; 5.0), of 8192 4.6; 6.9 (1024 4.3; 6.1).
+constexpr int64_t kUnits = 256;   // compute units
 template <typename T, int OUT>
 BlockPick pick(int cols, int64_t rows) {
   if (cols <= 512) return {block_norm_kernel<T, OUT, 64, 1>, 256, 4};
@@ -185,7 +187,7 @@ BlockPick pick(int cols, int64_t rows) {
   if (cols <= 2048) return {block_norm_kernel<T, OUT, 256, 1>, 256, 1};
   if (cols <= 4096) return {block_norm_kernel<T, OUT, 256, 2>, 256, 1};
   if (cols <= 8192) return {block_norm_kernel<T, OUT, 512, 2>, 512, 1};
-  if (cols <= 16384 && rows > 512) return {block_norm_kernel<T, OUT, 512, 4>, 512, 1};
+  if (cols <= 16384 && rows > kUnits) return {block_norm_kernel<T, OUT, 512, 4>, 512, 1};
   if (cols <= 16384) return {block_norm_kernel<T, OUT, 1024, 2>, 1024, 1};
   return {block_norm_kernel<T, OUT, 1024, 4>, 1024, 1};
 }

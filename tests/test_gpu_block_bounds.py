@@ -58,9 +58,11 @@ def test_norm_without_eps(cols, group, out):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,cols,group,gate", [(600, 16384, 0, "after"), (513, 8200, 0, "before"), (513, 8200, 1640, "after"),
-                                                  (520, 9216, 1152, "before"), (515, 16384, 4096, None), (514, 12288, 128, "after")])
+                                                  (520, 9216, 1152, "before"), (515, 16384, 4096, None), (514, 12288, 128, "after"),
+                                                  (257, 16384, 512, "after"), (256, 16384, 512, "after"), (300, 9000, 1800, "before")])
 def test_norm_of_many_long_rows(dtype, rows, cols, group, gate):
-    """More than 512 rows of 8193 to 16384 columns: 32 columns a thread, gate and residual read where they are used."""
+    """More rows than compute units, of 8193 to 16384 columns: 32 columns a thread, gate and residual read where they are
+    used; and as many."""
     compare(norm_case(rows, cols, dtype, group=group, gate=gate, seed=rows), out_dtype="f32")
 
 
