@@ -9,7 +9,7 @@
 // Bound by memory: every operand is read once and every result written once, a row
 // staying in registers between its sums and its output. Each part as a call of its own
 // would write u and h and read them again. 16384 x 2048 bf16 with a residual between
-// two norms (268 MB) takes 55 us, 4.9 TB/s, as much as a large copy; 16 rows of 4096,
+// two norms (268 MB) takes 53 to 55 us, 5 TB/s, as much as a large copy; 16 rows of 4096,
 // normed by heads of 128, gated, to E4M3 6.0 us, of which an empty launch is 4.6.
 #include <type_traits>
 
@@ -35,8 +35,8 @@ struct BlockArgs {
   int32_t wide;   // bits 0 to 5: x, gate, residual, y, weight, next_weight take 16-byte (codes: 8-byte) accesses
 };
 
-// e^-v is an infinity for v below about -88, and the quotient then zero, as which
-// both functions are stored
+// e^-v is an infinity for v below about -88, and the quotient then zero: sigmoid is
+// below fp32's normal numbers there, and silu's value, 2.4e-37 at most, is given as zero
 __device__ __forceinline__ float activate(float v, int act) {
   if (act == RSQ_ACT_NONE) return v;
   return (act == RSQ_ACT_SILU ? v : 1.f) / (1.f + expf(-v));
@@ -109,6 +109,9 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void block_norm_kernel(BlockArgs
 #pragma unroll
           for (int i = 0; i < NV; ++i) sums[i] += __shfl_xor(sums[i], s, 64);
       } else {
+        // Of any other group a thread adds up the sums of eight columns alone, which large groups
+        // pay for: 4096 rows of 16384 bf16 columns in groups of 1024 84 us, of 4096 237, of 16384
+        // 909, where groups of up to 512 and whole rows take 58.
         float* const p = part[R < 256 ? threadIdx.x / R : 0];
 #pragma unroll
         for (int i = 0; i < NV; ++i) p[i * R + tid] = sums[i];

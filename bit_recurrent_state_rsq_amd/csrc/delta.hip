@@ -10,9 +10,9 @@
 // follows the state through a sequence's chunks.
 //
 // 16384 tokens of 32 heads of 128 x 128 with 16 key heads (bf16, 411 MB, 60 GFLOP of the
-// recurrence's own operations: 80 us) take 511 to 523 us (by the card): 99 for the chunks, which is memory (32 KB
-// read, 25 written a chunk and head, 4.7 TB/s), and 410 for the chain of 256 chunks. A chunk of it
-// takes 1.6 us, three steps of about 1100 cycles: in the first the state's pieces come
+// recurrence's own operations: 80 us) take 520 to 540 us (by the card): 87 for the chunks, which is memory (32 KB
+// read, 25 written a chunk and head, 5.4 TB/s), and 436 for the chain of 256 chunks. A chunk of it
+// takes 1.7 us, three steps of about 1150 cycles: in the first the state's pieces come
 // through LDS (64 KB for eight wavefronts), in the second the products with T, in the third
 // the state's update and its splitting into pieces, each step with an LDS round trip and a
 // barrier; the products themselves are 800 cycles of a SIMD. A compute unit alone takes no
@@ -22,7 +22,7 @@
 // raised priority for the wavefronts that make U, T's pieces stored as such (511 -> 566:
 // more to read), a wavefront for 16 columns and all rows (no exchange, but 182 products and
 // 800 vector instructions one after another: 1.1 ms), parts of K S0 summed through LDS (744 us).
-// States keep 1.3e-7 of their norm; two pieces instead of three would leave 2.4e-6.
+// States keep 1.3e-7 to 1.5e-7 of their norm; two pieces instead of three would leave 2.4e-6.
 #include <algorithm>
 
 #include "chunk.hpp"
@@ -982,7 +982,11 @@ struct DeltaPlan {
 // bf16): the longest sequence takes its chunks one after another, and all that the
 // 256 compute units share. By the longer of the two, us, the first tiles chosen: 8192 tokens
 // of 32 heads one 301, two 382, four 613; of 64 heads two 477, one 555, four 662; of 128 four
-// 838, two 876, one 1041.
+// 838, two 876, one 1041. The same times decide for the other types and widths: of bf16 with d_k
+// 64, 128 and 256 and fp32 with 64 and 128, 4096 tokens of 16 to 128 heads, 8 and 16 prompts of 512
+// and 64 of 256, the tiles chosen were the fastest of all in each case, or within 2% of it (4096
+// tokens of 32 heads of 128 x 128 fp32 one 354, two 398; of 64 two 497, one 688; of 256 x 128 bf16
+// one 220, two 308, and two 347, one 430; of 64 x 64 bf16, 128 heads, two 226, one 278, four 315).
 template <typename T, int DK, int PI, int PY>
 void pick_delta(DeltaPlan& w, const rsq_linear_attn* p) {
   w.prepare = delta_prepare_kernel<T, DK, PI, PY>;
@@ -1042,7 +1046,9 @@ rsq_status run_delta(const rsq_linear_attn* p, const LinearArgs& l, void* stream
   a.keys = a.chunks + w.chunk_bytes;
   a.vblocks = (int32_t)w.vblocks, a.units = (int32_t)w.units;
   if (p->max_len > 0) {
-    // columns side by side where all sequences are short or there are few of them (a chunk takes the first only)
+    // Columns side by side where all sequences are short or there are few of them (a chunk takes the first only).
+    // One of 64 tokens and, of eight each, one (of 16 heads, 48 workgroups) 17 us so, 24 otherwise; four (of 32
+    // heads, 192) 28.5, 33; eight (352) 31, 36; 16 (640) 38, 42; but 32 (1216) 64.6, 62.
     const int64_t across = w.few || w.slots * p->heads <= 512 ? ceil_div(p->d_v, 64) : 1;
     hipLaunchKernelGGL(w.prepare, dim3((unsigned)(w.slots * p->heads), (unsigned)across), dim3(256), 0, (hipStream_t)stream, a);
     if (const rsq_status s = launched("delta rule, chunks")) return s;

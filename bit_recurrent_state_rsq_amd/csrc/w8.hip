@@ -327,16 +327,19 @@ struct W8Pick {
 //   to 1300              four tiles, eight wavefronts:  40 x 3000 x 1001 4.9, two and sixteen 6.1;
 //                        16 x 12352 x 2048 5.2, blocks of 64 x 64 7.3
 //   to 2600 (1800 where  32 rows of four tiles, four wavefronts: 256 x 2048 x 4096 8.9, blocks of 64 x 64
-//   rows are short)      11.7; 333 x 1031 x 705 6.4, 10.0; but 256 x 2049 x 1025 13.0, 10.0
+//   rows are short)      11.7; 333 x 1031 x 705 6.4, 10.0; 100 x 3700 x 1000 8.1, 8.8; 64 x 6400 x 2048
+//                        9.5, 10.5; but 256 x 1600 x 1024 7.0, 6.0; 270 x 1500 x 96 4.3, 3.8. Of short rows
+//                        above 1800: 333 x 1700 x 1024 7.7, 5.9; 256 x 2049 x 1025 13.4, 9.6; but 128 x 4096
+//                        x 2048 8.6, 10.0
 //   to 9000              blocks of 64 x 64:   128 x 12352 x 2048 10.3, of 64 x 128 11.9; 512 x 4096 x 4096 16.4, 18.3
 //   above                blocks of 64 x 128:  256 x 12352 x 2048 15.0, of 64 x 64 18.2
 // Before the last two come blocks of 128 x 256, three stages of 24 KB, two workgroups a compute
-// unit, where there are workgroups for three quarters of the units and rows of more than 1024: 4096 x
-// 12352 x 2048 115, of 64 x 128 142, of 256 x 256 165; 512 x 12352 x 2048 25.3, 29.6, 43; but 700 x
-// 7000 x 1024 (168 workgroups) 15.9, 13.4 and 4096 x 28672 x 1024 238, 224 (y is most of it);
-// and of 256 x 256 where rows are longer than 6144 and those blocks fill four fifths of the compute
-// units' rounds: 4096 x 28672 x 8192 882, of 128 x 256 954; 512 x 28672 x 8192 117, 138; but 4096 x
-// 8192 x 6144 197, 184.
+// unit, where there are 190 workgroups and more and rows of more than 1024: 4096 x 12352 x 2048 115,
+// of 64 x 128 142, of 256 x 256 165; 512 x 12352 x 2048 25.3, 29.6, 43 (of 160 to 192 workgroups with
+// rows of 2048 both take 26 to 28, within 2%); but 700 x 7000 x 1024 (168 workgroups) 15.9, 13.4 and
+// 4096 x 28672 x 1024 238, 224 (y is most of it); and of 256 x 256 where rows are longer than 6144 and
+// those blocks fill four fifths of the compute units' rounds: 4096 x 28672 x 8192 882, of 128 x 256
+// 954; 512 x 28672 x 8192 117, 138; but 4096 x 8192 x 6144 197, 184.
 W8Pick pick_w8(int64_t m, int tiles, int kblocks) {
   const int64_t mtiles = ceil_div(m, 16), work = mtiles * tiles;
   if (work <= 600 && kblocks > 32) return {w8_few_kernel<2, 1, 16>, 16, 2, 16, false};

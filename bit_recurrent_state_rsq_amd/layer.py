@@ -183,7 +183,8 @@ def block_norm(x, weight=None, gate=None, gate_first=False, activation="silu", g
     Parts whose operand is None are left out. weight: fp32 [cols], or [group] for all groups; gate and residual like x;
     activation: 'silu', 'sigmoid' or None. out_dtype: 'f32' or 'bf16' (default: x's type) returns y; 'int8' or 'e4m3'
     returns (codes, scales), one fp32 scale a row, or per `scale_group` columns. With a residual and neither
-    next_weight, out_dtype nor out, the new residual is the result, and y is not written apart from it."""
+    next_weight, out_dtype nor out, the new residual is the result, and y is not written apart from it. For the last
+    line alone, of x + residual, there is rms_norm."""
     return _run(_binding.block_norm, x, stream, x, weight, gate, gate_first, _choice(_GATES, activation, "activation"), group,
                 eps, residual, residual_scale, next_weight, _choice(_OUT, out_dtype, "out_dtype"), scale_group, out, scales)
 

@@ -464,6 +464,9 @@ rsq_status rsq_state_load(rsq_state* st, const float* dense, void* stream);
  * of its terms, before o is rounded to bf16); the state itself is exact to fp32. A v
  * that is not finite makes its column NaN from its token on, a k, alpha or beta (with
  * beta given) the whole head; earlier tokens are not touched.
+ * A call gives the same bits every time. The last bits of a sequence's o and state may
+ * differ with the number of heads and with what else is in the batch, which decide how
+ * the work is cut up, and so the order of sums.
  * rsq_linear_attention_step takes one row of every sequence: offsets NULL, max_len
  * 1; d_k <= 256; alpha and beta [seqs][heads].
  */
@@ -539,7 +542,9 @@ rsq_status rsq_rms_norm(const rsq_norm* norm, void* stream);
  *                without next_weight and codes (out_dtype is then not looked at
  *                beyond being a type)
  *   cols         at most 32768
- * The sums of squares are fp32, as in rsq_rms_norm.
+ * The sums of squares are fp32, as in rsq_rms_norm. With a residual and next_weight
+ * alone it is rsq_rms_norm's operation; of its own are the first norm, groups, gate and
+ * residual_scale. Of 8193 to 16384 columns the last bits may differ with the rows.
  */
 typedef struct rsq_block {
   int32_t dtype, out_dtype, cols, group, weight_cols, scale_group, activation, gate_first;

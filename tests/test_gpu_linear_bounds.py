@@ -152,3 +152,21 @@ def test_states_that_are_not_finite(dtype, tokens, delta):
     state[0, 1, :, 3] = state[1, 0, :, 39] = True
     assert not torch.isfinite(o[mask]).any() and torch.equal(o[~mask], o0[~mask]) and torch.equal(S[~state], S0[~state])
     assert not torch.isfinite(S[0, 1, 7, 3]) and torch.isnan(S[1, 0, 9, 39])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("what", ["k", "alpha"])
+@pytest.mark.parametrize("lengths", [[150, 90], [1500, 300]])
+def test_keys_and_decays_that_are_not_finite_without_the_delta_rule(dtype, what, lengths):
+    """Earlier tokens, other heads and other sequences keep their bits; from the token on the head's state is not finite."""
+    c = make(lengths, 2, 2, 64, 32, dtype, seed=7, delta=False)
+    args = lambda **kw: {"alpha": c["alpha"], "state": c["state"].clone(), "offsets": c["offsets"], "max_len": c["max_len"], **kw}  # noqa: E731
+    o0, S0 = rsq.linear_attention(c["q"], c["k"], c["v"], **args())
+    t = c[what].clone()
+    t[(100, 1, 3) if what == "k" else (100, 1)] = float("nan")
+    o, S = rsq.linear_attention(c["q"], t if what == "k" else c["k"], c["v"], **args(**({"alpha": t} if what == "alpha" else {})))
+    n = lengths[0]
+    assert torch.equal(o[:100], o0[:100]) and torch.equal(o[:, 0], o0[:, 0]) and torch.equal(o[n:], o0[n:])
+    assert torch.isnan(o[100:n, 1]).all()
+    assert torch.equal(S[0, 0], S0[0, 0]) and torch.equal(S[1], S0[1])
+    assert torch.isnan(S[0, 1] if what == "alpha" else S[0, 1, 3]).all()
